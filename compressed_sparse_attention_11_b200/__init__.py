@@ -8,7 +8,11 @@ All arithmetic runs in the library's CUDA kernels; there is no fallback.
 The functions carry the C names: ``csa_compress``, ``csa_index_topk``,
 ``csa_sparse_attn``, ``hca_attn`` and the decode-cache calls
 (``CsaCache`` wraps ``csa_cache_layout`` / ``csa_cache_store_entries`` /
-``csa_cache_write_rows`` / ``csa_decode_step``).
+``csa_cache_write_rows`` / ``csa_decode_step``), ``csa_qk_norm_rope``,
+``csa_window_attn``, the 4-bit key/value cache (``csa_kv4_cache``,
+``csa_kv4_store``, ``csa_kv4_fetch``, ``csa_kv4_decode_attn``) and the blocks
+of paged caches (``csa_blocks_copy``, ``csa_blocks_fork``,
+``csa_blocks_free``, ``csa_blocks_compact``).
 """
 from __future__ import annotations
 
@@ -37,6 +41,10 @@ EXPORTED = (
     "csa_grouped_out_proj_workspace", "csa_grouped_out_proj",
     "csa_paged_cache_layout", "csa_paged_cache_store_entries", "csa_paged_cache_write_rows",
     "csa_paged_decode_step",
+    "csa_qk_norm_rope", "csa_window_attn",
+    "csa_kv4_block_bytes", "csa_kv4_store", "csa_kv4_fetch", "csa_kv4_decode_workspace",
+    "csa_kv4_decode_attn",
+    "csa_blocks_copy", "csa_blocks_fork", "csa_blocks_free", "csa_blocks_compact",
 )
 CSA_INDEX_FP8_QK, CSA_INDEX_BF16_SCORES = 1, 2
 
@@ -79,6 +87,25 @@ class Paging(ctypes.Structure):
 class NormRope(ctypes.Structure):
     _fields_ = [("gamma", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("rope_dims", ctypes.c_int32), ("rope_base", ctypes.c_float)]
+
+
+class QkRope(ctypes.Structure):
+    _fields_ = [("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p),
+                ("per_head", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rope_dims", ctypes.c_int32), ("rope_base", ctypes.c_float),
+                ("halves", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4)]
+
+
+class Kv4Desc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("max_blocks", ctypes.c_int64),
+                ("num_blocks", ctypes.c_int64), ("nkv", ctypes.c_int32), ("c", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32)]
+
+
+class BlockRegion(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("block_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -135,6 +162,20 @@ def lib() -> ctypes.CDLL:
                                         vp, vp, vp, sz, vp]),
         "csa_grouped_out_proj_workspace": (sz, [i64, i32, i32]),
         "csa_grouped_out_proj": (i32, [vp, i64, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp, vp]),
+        "csa_qk_norm_rope": (i32, [vp, i64, vp, i64, i64, i32, i32, i32, vp,
+                                   ctypes.POINTER(QkRope), i32, vp, i64, vp, i64, vp]),
+        "csa_window_attn": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, vp, f32, i64, i64, i64, i32,
+                                  i32, i32, i32, vp, vp]),
+        "csa_kv4_block_bytes": (sz, [i32, i32, i32]),
+        "csa_kv4_store": (i32, [ctypes.POINTER(Kv4Desc), vp, i64, vp, vp, i64, vp, i64, i32, vp]),
+        "csa_kv4_fetch": (i32, [ctypes.POINTER(Kv4Desc), vp, i64, vp, i32, vp, vp, vp]),
+        "csa_kv4_decode_workspace": (sz, [i32, i32, i32]),
+        "csa_kv4_decode_attn": (i32, [ctypes.POINTER(Kv4Desc), vp, vp, i32, i64, i64, vp, f32, vp,
+                                      vp, sz, vp]),
+        "csa_blocks_copy": (i32, [ctypes.POINTER(BlockRegion), i32, i64, vp, vp, i64, vp, vp]),
+        "csa_blocks_fork": (i32, [vp, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]),
+        "csa_blocks_free": (i32, [vp, i64, i64, i64, vp, i32, vp, vp, vp, vp]),
+        "csa_blocks_compact": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, vp]),
         "csa_index_topk_lowp_workspace": (sz, [i64, i64, i32, i32, i32, i32, i32]),
         "csa_index_topk_lowp": (i32, [vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, i32, vp, vp,
                                       sz, vp]),
@@ -376,6 +417,321 @@ def csa_grouped_out_proj(o, w1, w2, ws: Optional[torch.Tensor] = None,
     return out
 
 
+# --------------------------------------- head norms, window, 4-bit cache, blocks ---
+
+class _On:
+    """Makes a tensor's device the current one around a call that asks for the device."""
+
+    def __init__(self, t: torch.Tensor):
+        self.guard = None if t.device.index == torch.cuda.current_device() else \
+            torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _dev_ptr(t: Optional[torch.Tensor], like: torch.Tensor, dtype, name: str, numel=None):
+    """Pointer of a dense tensor of the given type on ``like``'s device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must live on {like.device}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements")
+    return _ptr(t)
+
+
+def _tokens_view(x: torch.Tensor, name: str):
+    """(tokens, stride) of x [..., heads, c] whose heads are dense and whose
+    leading dims step by one token stride (elements)."""
+    if not x.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    shape, strides = x.shape, x.stride()
+    heads, c = shape[-2], shape[-1]
+    if (c > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != c):
+        raise ValueError(f"the heads of {name} must be dense")
+    tokens, step = 1, 0
+    for size, st in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+        if size == 1:
+            continue
+        if tokens == 1:
+            step = st
+        elif st != step * tokens:
+            raise ValueError(f"the tokens of {name} must step by one stride")
+        tokens *= size
+    if 0 in shape:
+        tokens = 0
+    return tokens, (step if tokens > 1 else heads * c)
+
+
+def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EPS,
+                     rope_dims: int = 64, rope_base: float = ROPE_BASE, halves: bool = False,
+                     sections=None, q_out: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None):
+    """RMSNorm (weight [c], or [heads, c] for one per head; None: no norm) and
+    rotation of the trailing dims of q [..., nh, c] and k [..., nkv, c] in one
+    pass; either may be None.  ``pos``: int64 [...] as the leading dims, or
+    [axes, ...] with ``sections`` = the pairs of each axis.  q and k may be
+    views with one token stride (of a packed projection); q_out and k_out may
+    be q and k.  Returns (q_out, k_out)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    c, dt = ref.shape[-1], _dt(ref)
+    args, tokens = [], None
+    for x, out, gamma, name in ((q, q_out, q_gamma, "q"), (k, k_out, k_gamma, "k")):
+        if x is None:
+            args.append((None, c, None, c, 0, None))
+            continue
+        if x.dtype != ref.dtype or x.device != ref.device or x.shape[-1] != c:
+            raise ValueError("q and k must have one dtype, device and head dim")
+        heads = x.shape[-2]
+        n, step = _tokens_view(x, name)
+        if tokens is not None and n != tokens:
+            raise ValueError("q and k must have the same tokens")
+        tokens = n
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+            raise ValueError(f"{name}_out must be like {name}")
+        gp = None
+        if gamma is not None:
+            if tuple(gamma.shape) not in ((c,), (heads, c)):
+                raise ValueError(f"{name}_gamma must be [c] or [heads, c]")
+            gp = _dev_ptr(gamma, ref, torch.float32, f"{name}_gamma")
+        args.append((x.data_ptr(), step, out, _tokens_view(out, f"{name}_out")[1], heads, gp))
+    dims = {g.dim() for x, g in ((q, q_gamma), (k, k_gamma)) if x is not None and g is not None}
+    if len(dims) == 2:
+        raise ValueError("q_gamma and k_gamma must both be [c] or both be [heads, c]")
+    if sections is None:
+        sections = (rope_dims // 2,)
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("1 to 4 sections")
+    pp = None
+    if rope_dims > 0:
+        pp = _dev_ptr(pos, ref, torch.int64, "pos", len(sections) * tokens)
+    (qp, qs, qo, qos, nh, qg), (kp, ks, ko, kos, nkv, kg) = args
+    p = QkRope(qg, kg, 1 if dims == {2} else 0, float(eps), int(rope_dims), float(rope_base),
+               1 if halves else 0, len(sections), (ctypes.c_int32 * 4)(*sections))
+    with _On(ref):
+        _check(lib().csa_qk_norm_rope(qp, qs, kp, ks, tokens, nh, nkv, c, pp, ctypes.byref(p), dt,
+                                      None if qo is None else qo.data_ptr(), qos,
+                                      None if ko is None else ko.data_ptr(), kos, _stream(ref)))
+    return qo, ko
+
+
+def csa_window_attn(q, k, v, window: int, first: int = 0, sink=None, scale: float = 1.0,
+                    out: Optional[torch.Tensor] = None):
+    """Causal attention over the last ``window`` tokens and the first ``first``
+    ones: q [B, n_q, nh, c], k and v [B, n_k, nkv, c] (query i at position
+    n_k - n_q + i; views with one token stride), or v None and k [B, n, c]:
+    shared rows, each its own value.  Returns [B, n_q, nh, c]."""
+    if v is None and k.dim() == 3:
+        k = k.unsqueeze(2)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, n_q, nh, c] and k [B, n_k, nkv, c]")
+    B, nq, nh, c = q.shape
+    nk, nkv = k.shape[1], k.shape[2]
+    for x, name in ((k, "k"), (v, "v")):
+        if x is not None and (tuple(x.shape) != (B, nk, nkv, c) or x.dtype != q.dtype
+                              or x.device != q.device):
+            raise ValueError(f"{name} must be [B, n_k, nkv, c] of q's dtype and device")
+    if out is None:
+        out = torch.empty((B, nq, nh, c), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (B, nq, nh, c) or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError("out must be like q")
+    qs, ks = _tokens_view(q, "q")[1], _tokens_view(k, "k")[1]
+    vs = 0 if v is None else _tokens_view(v, "v")[1]
+    sp = _dev_ptr(sink, q, torch.float32, "sink", nh)
+    with _On(q):
+        _check(lib().csa_window_attn(q.data_ptr(), qs, k.data_ptr(), ks,
+                                     None if v is None else v.data_ptr(), vs, int(window),
+                                     int(first), sp, float(scale), B, nq, nk, nh, nkv, c, _dt(q),
+                                     _ptr(out), _stream(q)))
+    return out
+
+
+def csa_kv4_block_bytes(nkv: int, c: int, block_tokens: int = 128) -> int:
+    return int(lib().csa_kv4_block_bytes(nkv, c, block_tokens))
+
+
+def csa_kv4_cache(num_blocks: int, nkv: int, c: int, block_tokens: int = 128,
+                  device="cuda") -> torch.Tensor:
+    """An empty 4-bit key/value cache: uint8 [num_blocks, nkv, block_tokens / 16, 18 c + 32]
+    (c = 64 or 128)."""
+    n = csa_kv4_block_bytes(nkv, c, block_tokens)
+    if n == 0:
+        raise ValueError("c must be 64 or 128, nkv >= 1 and block_tokens a multiple of 16")
+    return torch.zeros((num_blocks, nkv, block_tokens // 16, 18 * c + 32), dtype=torch.uint8,
+                       device=device)
+
+
+def _kv4_desc(cache: torch.Tensor, block_table: torch.Tensor) -> Kv4Desc:
+    if cache.dtype != torch.uint8 or cache.dim() != 4:
+        raise ValueError("cache must be a uint8 [num_blocks, nkv, block_tokens / 16, bytes] tensor")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 [batch, max_blocks] tensor")
+    nb, nkv, tiles, by = cache.shape
+    return Kv4Desc(_ptr(cache), _dev_ptr(block_table, cache, torch.int32, "block_table"),
+                   block_table.shape[0], block_table.shape[1], nb, nkv, (by - 32) // 18,
+                   16 * tiles)
+
+
+def _kv4_pos(d: Kv4Desc, cache, pos, count):
+    return (_dev_ptr(pos, cache, torch.int64, "pos", d.batch),
+            _dev_ptr(count, cache, torch.int32, "count", d.batch))
+
+
+def csa_kv4_store(cache, block_table, pos, k, v, count: Optional[torch.Tensor] = None):
+    """Stores k and v [B, n, nkv, c] (bf16 or fp32, views with one token
+    stride) in 4 bits at positions pos[b] + i; count: int32 [B] rows to store."""
+    d = _kv4_desc(cache, block_table)
+    for x, name in ((k, "k"), (v, "v")):
+        if x.dim() != 4 or x.shape[0] != d.batch or tuple(x.shape[2:]) != (d.nkv, d.c) \
+                or x.shape != k.shape or x.dtype != k.dtype or x.device != cache.device:
+            raise ValueError(f"{name} must be [batch, n, nkv, c] on the cache's device")
+    pp, cp = _kv4_pos(d, cache, pos, count)
+    ks, vs = _tokens_view(k, "k")[1], _tokens_view(v, "v")[1]
+    with _On(cache):
+        _check(lib().csa_kv4_store(ctypes.byref(d), pp, k.shape[1], cp, k.data_ptr(), ks,
+                                   v.data_ptr(), vs, _dt(k), _stream(cache)))
+
+
+def csa_kv4_fetch(cache, block_table, pos, n: int, count: Optional[torch.Tensor] = None,
+                  dtype=torch.bfloat16):
+    """The stored rows of positions pos[b] .. pos[b] + n - 1 as k, v [B, n, nkv, c]
+    (zeros from row count[b] on and where the block is absent)."""
+    d = _kv4_desc(cache, block_table)
+    pp, cp = _kv4_pos(d, cache, pos, count)
+    k = torch.empty((d.batch, n, d.nkv, d.c), dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    with _On(cache):
+        _check(lib().csa_kv4_fetch(ctypes.byref(d), pp, n, cp, _dt(k), _ptr(k), _ptr(v),
+                                   _stream(cache)))
+    return k, v
+
+
+def csa_kv4_decode_workspace(nh: int, nkv: int, c: int) -> int:
+    return int(lib().csa_kv4_decode_workspace(nh, nkv, c))
+
+
+def csa_kv4_decode_attn(q, cache, block_table, pos, scale: float, window: int = 0, first: int = 0,
+                        sink=None, ws: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None):
+    """Attention of one query token per sequence, q [B, nh, c] bf16 at position
+    pos[b] (already stored), over the 4-bit cache: every token, or with
+    ``window`` the last ``window`` and the first ``first`` ones."""
+    d = _kv4_desc(cache, block_table)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != d.batch or q.shape[2] != d.c \
+            or q.device != cache.device:
+        raise ValueError("q must be a bfloat16 [batch, nh, c] tensor on the cache's device")
+    nh = q.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError("out must be like q")
+    pp, _ = _kv4_pos(d, cache, pos, None)
+    sp = _dev_ptr(sink, q, torch.float32, "sink", nh)
+    with _On(cache):
+        if ws is None:
+            ws = torch.empty(max(csa_kv4_decode_workspace(nh, d.nkv, d.c), 16), dtype=torch.uint8,
+                             device=q.device)
+        _check(lib().csa_kv4_decode_attn(ctypes.byref(d), pp, _ptr(q), nh, int(window), int(first),
+                                         sp, float(scale), _ptr(out), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(q)))
+    return out
+
+
+def csa_blocks_copy(regions, src, dst, count: Optional[torch.Tensor] = None):
+    """In every region (a dense tensor [num_blocks, ...]) block dst[i] becomes a
+    copy of block src[i] (int32 lists on the device; ids outside the pool are
+    skipped; count: int32, count[0] pairs).  No block may be a destination
+    twice, nor both a source and a destination."""
+    regions = list(regions)
+    if not regions:
+        return
+    if len(regions) > 16:
+        raise ValueError("at most 16 regions")
+    nb, ref = regions[0].shape[0], regions[0]
+    arr = (BlockRegion * len(regions))()
+    for i, r in enumerate(regions):
+        if r.shape[0] != nb or r.device != ref.device:
+            raise ValueError("regions must have the same blocks and device")
+        arr[i].base = _ptr(r)
+        arr[i].block_bytes = r.numel() // max(nb, 1) * r.element_size()
+    n = src.numel()
+    sp, dp = (_dev_ptr(x, ref, torch.int32, nm, n) for x, nm in ((src, "src"), (dst, "dst")))
+    cp = _dev_ptr(count, ref, torch.int32, "count")
+    with _On(ref):
+        _check(lib().csa_blocks_copy(arr, len(regions), nb, sp, dp, n, cp, _stream(ref)))
+
+
+def _table(table: torch.Tensor, out: Optional[torch.Tensor]):
+    if table.dim() != 2 or table.dtype != torch.int32:
+        raise ValueError("table must be an int32 [rows, max_blocks] tensor")
+    if out is None:
+        out = torch.empty_like(table, memory_format=torch.contiguous_format)
+    elif out.shape != table.shape:
+        raise ValueError("table_out must be like table")
+    return _ptr(table), table.shape[0], table.shape[1], \
+        _dev_ptr(out, table, torch.int32, "table_out"), out
+
+
+def csa_blocks_fork(table, src, dst, tokens, fresh, block_tokens: int = 128,
+                    table_out: Optional[torch.Tensor] = None):
+    """Row dst[i] of the new table forks the first tokens[i] (int64) tokens of row
+    src[i]: whole blocks are shared, a partly filled last block becomes
+    fresh[i].  Returns (table_out, copy_src, copy_dst); the copies (for
+    csa_blocks_copy, once per cache) are -1 where there is nothing to copy."""
+    tp, rows, mb, op, out = _table(table, table_out)
+    n = src.numel()
+    cs = torch.empty(n, dtype=torch.int32, device=table.device)
+    cd = torch.empty_like(cs)
+    ptrs = [_dev_ptr(x, table, dt, nm, n) for x, dt, nm in (
+        (src, torch.int32, "src"), (dst, torch.int32, "dst"), (tokens, torch.int64, "tokens"),
+        (fresh, torch.int32, "fresh"))]
+    with _On(table):
+        _check(lib().csa_blocks_fork(tp, rows, mb, *ptrs, n, int(block_tokens), op, _ptr(cs),
+                                     _ptr(cd), _stream(table)))
+    return out, cs, cd
+
+
+def csa_blocks_free(table, seqs, num_blocks: int, table_out: Optional[torch.Tensor] = None):
+    """Rows ``seqs`` (int32) of the new table are -1.  Returns (table_out, freed,
+    nfreed): the blocks no row names any more, ascending (int32 [num_blocks],
+    -1 padded), and how many (int32 [1])."""
+    tp, rows, mb, op, out = _table(table, table_out)
+    freed = torch.empty(num_blocks, dtype=torch.int32, device=table.device)
+    n = torch.empty(1, dtype=torch.int32, device=table.device)
+    sp = _dev_ptr(seqs, table, torch.int32, "seqs")
+    with _On(table):
+        _check(lib().csa_blocks_free(tp, rows, mb, num_blocks, sp, seqs.numel(), op, _ptr(freed),
+                                     _ptr(n), _stream(table)))
+    return out, freed, n
+
+
+def csa_blocks_compact(table, num_blocks: int, table_out: Optional[torch.Tensor] = None):
+    """The blocks in use move to the low end of the pool.  Returns (table_out,
+    copy_src, copy_dst, counts): the moves (int32 [num_blocks], -1 padded; for
+    csa_blocks_copy with count=counts, once per cache) and counts = [moves,
+    blocks in use]."""
+    tp, rows, mb, op, out = _table(table, table_out)
+    cs = torch.empty(num_blocks, dtype=torch.int32, device=table.device)
+    cd = torch.empty_like(cs)
+    counts = torch.empty(2, dtype=torch.int32, device=table.device)
+    with _On(table):
+        _check(lib().csa_blocks_compact(tp, rows, mb, num_blocks, op, _ptr(cs), _ptr(cd),
+                                        _ptr(counts), _stream(table)))
+    return out, cs, cd, counts
+
+
 # ------------------------------------------------------------------- decode ---
 
 class CsaCache:
@@ -445,6 +801,38 @@ class CsaCache:
             g[~ok] = 0
             res[k] = g
         return res
+
+    def copy_blocks(self, src, dst, count: Optional[torch.Tensor] = None):
+        """Copies blocks of the paged pool (csa_blocks_copy over every entry region)."""
+        if self.paging is None:
+            raise ValueError("only a paged cache has blocks")
+        d, nb = self.desc, self.paging.num_blocks
+        epb = self.paging.block_tokens // d.m
+        regions = [self.region("entry_fp8", torch.uint8, (nb, epb * (d.c - d.rope_dims))),
+                   self.region("entry_scale", torch.float32, (nb, epb)),
+                   self.region("entry_rope", torch.bfloat16, (nb, epb * d.rope_dims))]
+        if not d.is_hca:
+            regions += [self.region("ikey_fp8", torch.uint8, (nb, epb * d.c_i)),
+                        self.region("ikey_scale", torch.float32, (nb, epb))]
+        csa_blocks_copy(regions, src, dst, count)
+
+    def copy_sequences(self, src, dst, count: Optional[torch.Tensor] = None):
+        """Copies what the cache keeps per sequence (window ring and compressor
+        state; without paging the entries too) of sequences src to dst."""
+        d, B = self.desc, self.desc.batch
+        regions = [self.region("window", torch.bfloat16, (B, d.window * d.c)),
+                   self.region("state", torch.bfloat16, (B, (2 if d.is_hca else 8) * d.m * d.c))]
+        if not d.is_hca:
+            regions.append(self.region("istate", torch.bfloat16, (B, 8 * d.m * d.c_i)))
+        if self.paging is None:
+            cap = d.capacity
+            regions += [self.region("entry_fp8", torch.uint8, (B, cap * (d.c - d.rope_dims))),
+                        self.region("entry_scale", torch.float32, (B, cap)),
+                        self.region("entry_rope", torch.bfloat16, (B, cap * d.rope_dims))]
+            if not d.is_hca:
+                regions += [self.region("ikey_fp8", torch.uint8, (B, cap * d.c_i)),
+                            self.region("ikey_scale", torch.float32, (B, cap))]
+        csa_blocks_copy(regions, src, dst, count)
 
     def store_entries(self, first: int, kv, ikey=None):
         count = kv.shape[1]

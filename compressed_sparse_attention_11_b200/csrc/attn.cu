@@ -11,6 +11,10 @@
 // "Core formulas chapter"; one softmax for window, compressed entries and
 // sink, as the reader's notes stress in section 1).
 //
+// With first >= 0 (window attention over the rows themselves: kv_comp =
+// kv_win, m = 1) the compressed part of E_t is the rows 0 .. first - 1 that
+// lie before the window.
+//
 // One block = one query x 8 heads (one warp per head).  Entries are gathered
 // 32 at a time into shared memory; the softmax is online (running max/sum per
 // head) in the log2 domain (q is pre-scaled by scale*log2(e)).
@@ -28,7 +32,7 @@ template <typename T>
 __global__ void __launch_bounds__(kAttnThreads) attn_kernel(
     const T* __restrict__ q, const T* __restrict__ kv_comp, const int32_t* __restrict__ idx,
     int k, const T* __restrict__ kv_win, int window, const float* __restrict__ sink,
-    float scale, int64_t n, int nh, int c, int m, int64_t E, QNormRope qn,
+    float scale, int64_t n, int nh, int c, int m, int64_t E, int64_t first, QNormRope qn,
     T* __restrict__ out) {
   extern __shared__ float smem[];
   const int ld = c + 1;
@@ -40,8 +44,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t = blockIdx.x, b = blockIdx.z;
   const int h0 = blockIdx.y * kAttnHG;
-  const int64_t V = min((t + 1) / m, E);
   const int64_t w0 = max((int64_t)0, t - window + 1);
+  const int64_t V = first >= 0 ? min(first, w0) : min((t + 1) / m, E);
   const int64_t n_comp = idx ? (int64_t)k : V;   // compressed slots
   const int64_t N = n_comp + (t - w0 + 1);       // total slots
 
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(
 cudaError_t launch_attn(const void* q, const void* kv_comp, const int32_t* idx, int k,
                         const void* kv_win, int window, const float* sink, float scale,
                         int64_t batch, int64_t n, int nh, int c, int m, csa_dtype dt,
-                        const csa_norm_rope* q_nr, void* out, cudaStream_t s) {
+                        const csa_norm_rope* q_nr, void* out, cudaStream_t s, int64_t first) {
   const int64_t E = n / m;
   const QNormRope qn = q_nr != nullptr
                            ? QNormRope{q_nr->gamma, q_nr->eps, q_nr->rope_dims, q_nr->rope_base}
@@ -182,8 +186,8 @@ cudaError_t launch_attn(const void* q, const void* kv_comp, const int32_t* idx, 
                         qn.gamma != nullptr ? qn.rope_dims : 0)) {
     unsigned int* err = device_timeout_flag();
     if (err == nullptr) return cudaErrorUnknown;
-    return launch_attn_tc(q, kv_comp, idx, k, kv_win, window, sink, scale, batch, n, m, qn, out,
-                          err, s);
+    return launch_attn_tc(q, kv_comp, idx, k, kv_win, window, sink, scale, batch, n, m, first, qn,
+                          out, err, s);
   }
   const size_t smem = sizeof(float) * ((size_t)kAttnTE * (c + 1) + (size_t)kAttnHG * c +
                                        kAttnHG * kAttnTE) + sizeof(int64_t) * kAttnTE;
@@ -193,13 +197,13 @@ cudaError_t launch_attn(const void* q, const void* kv_comp, const int32_t* idx, 
     cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     kern<<<grid, kAttnThreads, smem, s>>>((const float*)q, (const float*)kv_comp, idx, k,
                                           (const float*)kv_win, window, sink, scale, n, nh, c,
-                                          m, E, qn, (float*)out);
+                                          m, E, first, qn, (float*)out);
   } else {
     auto kern = attn_kernel<__nv_bfloat16>;
     cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     kern<<<grid, kAttnThreads, smem, s>>>(
         (const __nv_bfloat16*)q, (const __nv_bfloat16*)kv_comp, idx, k,
-        (const __nv_bfloat16*)kv_win, window, sink, scale, n, nh, c, m, E, qn,
+        (const __nv_bfloat16*)kv_win, window, sink, scale, n, nh, c, m, E, first, qn,
         (__nv_bfloat16*)out);
   }
   return cudaGetLastError();

@@ -10,6 +10,10 @@
 // context"; B9 of the "Core formulas chapter"; one softmax shared by the
 // window, the compressed entries and the sink).
 //
+// With first >= 0 (window attention over the rows themselves: kv_comp =
+// kv_win, m = 1) the entries are the rows 0 .. first - 1 that lie before the
+// window.
+//
 // Heads on TMEM lanes, 64 rows (M = 64): the 64 heads of one query take the
 // M side of both products and the N side is as wide as the operands allow:
 //   S[h, e]  = Q[h, :] . K[e, :]           M = 64 heads, N = 128 entries
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kv_comp,
     const int32_t* __restrict__ idx, int k, const __nv_bfloat16* __restrict__ kv_win,
     int window, const float* __restrict__ sink, float scale, int64_t n, int m, int64_t E,
-    int64_t total, QNormRope qn, __nv_bfloat16* __restrict__ out, unsigned int* __restrict__ err) {
+    int64_t first, int64_t total, QNormRope qn, __nv_bfloat16* __restrict__ out, unsigned int* __restrict__ err) {
   using namespace sm100;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -247,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
       const int64_t qi = blockIdx.x + kq * gridDim.x;
       if (qi >= total) break;
       const int64_t b = qi / n, t = qi % n;
-      const int64_t V = min((t + 1) / m, E);
       const int64_t w0 = max((int64_t)0, t - window + 1);
+      const int64_t V = first >= 0 ? min(first, w0) : min((t + 1) / m, E);
       const int nwin = (int)(t - w0 + 1);
       // the next query of this CTA (64 KB, contiguous) starts moving into L2
       if (ptid == 0 && qi + gridDim.x < total)
@@ -693,8 +697,8 @@ bool attn_tc_supported(int nh, int c, int k, csa_dtype dt, const void* q, const 
 
 cudaError_t launch_attn_tc(const void* q, const void* kv_comp, const int32_t* idx, int k,
                            const void* kv_win, int window, const float* sink, float scale,
-                           int64_t batch, int64_t n, int m, const QNormRope& qn, void* out,
-                           unsigned int* err, cudaStream_t s) {
+                           int64_t batch, int64_t n, int m, int64_t first, const QNormRope& qn,
+                           void* out, unsigned int* err, cudaStream_t s) {
   auto kern = qn.gamma != nullptr ? attn_tc_kernel<true> : attn_tc_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
@@ -702,7 +706,7 @@ cudaError_t launch_attn_tc(const void* q, const void* kv_comp, const int32_t* id
   const int64_t grid = std::min<int64_t>(total, sm_count());
   kern<<<(unsigned)grid, kThreads, SMEM, s>>>(
       (const __nv_bfloat16*)q, (const __nv_bfloat16*)kv_comp, idx, k,
-      (const __nv_bfloat16*)kv_win, window, sink, scale, n, m, n / m, total, qn,
+      (const __nv_bfloat16*)kv_win, window, sink, scale, n, m, n / m, first, total, qn,
       (__nv_bfloat16*)out, err);
   return cudaGetLastError();
 }

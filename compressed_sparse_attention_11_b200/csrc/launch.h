@@ -81,8 +81,8 @@ struct QNormRope {
 };
 cudaError_t launch_attn_tc(const void* q, const void* kv_comp, const int32_t* idx, int k,
                            const void* kv_win, int window, const float* sink, float scale,
-                           int64_t batch, int64_t n, int m, const QNormRope& qn, void* out,
-                           unsigned int* err, cudaStream_t s);
+                           int64_t batch, int64_t n, int m, int64_t first, const QNormRope& qn,
+                           void* out, unsigned int* err, cudaStream_t s);
 
 // tcgen05 decode indexer over FP8 keys (c_i = 128, nh_i in {64, 128}), persistent.
 struct CacheView;
@@ -188,11 +188,14 @@ cudaError_t launch_topk_rows(const float* scores, int64_t ld, int64_t batch, int
 
 // q_nr != NULL: each query head RMSNorm-ed and rotated for position t before
 // the logits, and the output's trailing dims rotated by -t (the entries are
-// taken as given: already normed and rotated).
+// taken as given: already normed and rotated).  first >= 0: window attention
+// (kv_comp = kv_win, m = 1, no idx), rows 0 .. first - 1 before the window
+// take the compressed entries' place.
 cudaError_t launch_attn(const void* q, const void* kv_comp, const int32_t* idx, int k,
                         const void* kv_win, int window, const float* sink, float scale,
                         int64_t batch, int64_t n, int nh, int c, int m, csa_dtype dt,
-                        const csa_norm_rope* q_nr, void* out, cudaStream_t s);
+                        const csa_norm_rope* q_nr, void* out, cudaStream_t s,
+                        int64_t first = -1);
 
 // Grouped output projection: z = grouped o W1^T (bf16 [rows, G dg]), y = z W2^T.
 cudaError_t launch_grouped_out_proj(const void* o, int64_t rows, int nh, int c, int G, int dg,

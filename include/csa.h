@@ -431,6 +431,182 @@ csa_status csa_paged_decode_step(const csa_cache_desc* desc, const csa_paging* p
                                  const void* q_i, const float* w_i, void* out, void* ws,
                                  size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * csa_qk_norm_rope -- RMSNorm of every query and key head and the position
+ * rotation, both tensors in one pass (csa_norm_rope_rows for heads that
+ * share no position rule or weight).  For each head row x of token t:
+ *   y = x / sqrt(mean(x^2) + eps) * gamma    (gamma NULL: y = x)
+ *   pair j of the trailing R = rope_dims dims turns by
+ *   pos[axis(j)][t] * rope_base^(-2j/R),  j < R/2
+ * pair j: dims (c - R + 2j, c - R + 2j + 1), or with `halves`
+ * (c - R + j, c - R/2 + j).  The first sections[0] pairs take the positions
+ * of axis 0, the next sections[1] those of axis 1, ... (text: one axis;
+ * images and video: time, height, width).  Positions may be negative.
+ *
+ *   q : tokens x [nh, c] of `dt`, q_stride elements from token to token (a
+ *       view of a packed projection's output); k : tokens x [nkv, c]
+ *   pos : [axes][tokens] int64 (device; unused when rope_dims = 0)
+ *   q_out, k_out : like q and k with strides of their own; a pointer may equal
+ *       its input with the same stride (in place), and must not overlap
+ *       another tensor of the call otherwise
+ *   nh = 0 or nkv = 0 leaves that tensor out (its pointers are ignored).
+ * Needs c <= 512 (above 256: c % 16 == 0); the halves form rope_dims % 16 == 0
+ * (% 32 above c = 256), else CSA_ERR_UNSUPPORTED.  Strides: whole 16-byte
+ * units.  Norm, angle (double) and rotation in fp32, one rounding to `dt`.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const float* q_gamma; /* [c], or [nh][c] with per_head; NULL: no norm of q   */
+  const float* k_gamma; /* [c], or [nkv][c] with per_head; NULL: no norm of k  */
+  int32_t per_head;     /* 0 or 1                                              */
+  float eps;            /* >= 0, finite                                        */
+  int32_t rope_dims;    /* R: 0 <= R <= c, R % 8 == 0 (0: no rotation)         */
+  float rope_base;      /* > 1 and finite                                      */
+  int32_t halves;       /* 0: neighbouring dims form a pair, 1: j and j + R/2  */
+  int32_t axes;         /* 1 .. 4                                              */
+  int32_t sections[4];  /* pairs of each axis, adding up to R/2                */
+} csa_qk_rope;
+csa_status csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            int64_t tokens, int nh, int nkv, int c, const int64_t* pos,
+                            const csa_qk_rope* p, csa_dtype dt, void* q_out, int64_t q_out_stride,
+                            void* k_out, int64_t k_out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * csa_window_attn -- causal attention of each query over a sliding window
+ * and the first tokens of its sequence, which stay visible:
+ *   E_t = { u <= t : u > t - window or u < first }
+ *   out[t, h] = sum_u e^{l_u} v[u, h'] / (e^{sink[h]} + sum_u e^{l_u}),
+ *   l_u = scale q[t, h] . k[u, h'],  h' = h / (nh / nkv)
+ * with query i at position t = n_k - n_q + i (n_q < n_k: a chunk of a prompt
+ * whose earlier keys and values are given).  sink NULL: no sink term.
+ *   q : [batch, n_q, nh, c]   k, v : [batch, n_k, nkv, c]   out : dense
+ *       [batch, n_q, nh, c]; token strides in elements, batch strides n_q
+ *       and n_k times those
+ *   v NULL: shared rows, each key row is its own value (nkv = 1, n_q = n_k,
+ *       dense) -- the window-only layers of the CSA / HCA stack
+ * Needs: separate values: bf16, c = 64 or 128; shared rows: c % 32 == 0 and
+ * c <= 512, fp32 or bf16 (64 heads x 512 on the tensor cores).  Else
+ * CSA_ERR_UNSUPPORTED.  out must not overlap an input.
+ * ------------------------------------------------------------------------ */
+csa_status csa_window_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, int64_t window, int64_t first,
+                           const float* sink, float scale, int64_t batch, int64_t n_q,
+                           int64_t n_k, int nh, int nkv, int c, csa_dtype dt, void* out,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * Keys and values held in 4 bits, in blocks behind a block table like the
+ * paged classical cache's: token u of sequence b is row u % block_tokens of
+ * block block_table[b][u / block_tokens].  A row (one token of one head, K or
+ * V) of c values x is stored as
+ *   E (one byte): the exponent byte of max|x| as fp32, less 10, in 1 .. 254,
+ *     or 255 when a value of the row is not finite (it then reads as NaN);
+ *     r = 2^(E - 127)
+ *   s (E4M3) for each 16 values: max|x| of them / (7 r)
+ *   code (4 bits): x / (s r) rounded to nearest even, in -7 .. 7 (0 if s = 0),
+ *     stored as code + 8;            the row's values are r s code.
+ * All steps in fp32.  A block holds [nkv][block_tokens / 16] images of 16
+ * tokens, 18 c + 32 bytes each:
+ *   K codes [slot][c/2], V codes [h][8][t][c/32][b][2], K scales [slot][c/16],
+ *   V scales [c/16][16 tokens], E [slot][K, V]
+ * for token 4t + 2h + b of the image (t < 4, h, b < 2), slot 8h + 2t + b; a K
+ * byte holds dims 2i (low) and 2i + 1, V bytes are indexed by the dims'
+ * eighth, 4-dim group and byte in it.  (The order in which the attention's
+ * matrix instructions take the rows.)
+ * Rows whose block is absent (not in [0, num_blocks), or behind the table)
+ * are not written, read as zeros by csa_kv4_fetch and are invisible to
+ * csa_kv4_decode_attn.  The same block must not be written for two tokens of
+ * one call.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* data;                 /* device: num_blocks * csa_kv4_block_bytes(...)    */
+  const int32_t* block_table; /* device [batch][max_blocks] int32                 */
+  int64_t batch;              /* sequences, <= 4096                               */
+  int64_t max_blocks;         /* block-table row length                           */
+  int64_t num_blocks;         /* blocks in the pool                               */
+  int32_t nkv;                /* key/value heads                                  */
+  int32_t c;                  /* head dim: 64 or 128                              */
+  int32_t block_tokens;       /* tokens per block, a positive multiple of 16      */
+} csa_kv4_cache;
+
+/* Bytes of one block; 0 for sizes that are not supported. */
+size_t csa_kv4_block_bytes(int nkv, int c, int block_tokens);
+
+/* Stores rows i < min(n, count[b]) of sequence b at positions pos[b] + i
+ * (device int64 [batch]; a negative pos[b] stores nothing; count: device int32
+ * [batch], NULL: n rows each).
+ *   k, v : [batch, n, nkv, c] of `dt`, token strides in elements (whole
+ *          16-byte units), batch strides n times those */
+csa_status csa_kv4_store(const csa_kv4_cache* cache, const int64_t* pos, int64_t n,
+                         const int32_t* count, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, csa_dtype dt, void* stream);
+
+/* The stored values back, as k, v [batch, n, nkv, c] of `dt` (exact in bf16
+ * and fp32): row i is position pos[b] + i; rows i >= count[b], of a negative
+ * pos[b] or of absent blocks are zeros. */
+csa_status csa_kv4_fetch(const csa_kv4_cache* cache, const int64_t* pos, int64_t n,
+                         const int32_t* count, csa_dtype dt, void* k, void* v, void* stream);
+
+/* Workspace bytes of csa_kv4_decode_attn on the current device. */
+size_t csa_kv4_decode_workspace(int nh, int nkv, int c);
+
+/* One query token per sequence, at position pos[b] (already stored; device
+ * int64 [batch]; a negative pos[b] gives zeros), over the cache:
+ *   E_b = { u <= pos[b] : u > pos[b] - window or u < first }, window = 0: all;
+ * the softmax, sink and heads as csa_window_attn.  A sequence that sees no row
+ * gives zeros.  q, out : [batch, nh, c] bf16.  ws: scratch of this call alone
+ * until it has finished on the stream. */
+csa_status csa_kv4_decode_attn(const csa_kv4_cache* cache, const int64_t* pos, const void* q,
+                               int nh, int64_t window, int64_t first, const float* sink,
+                               float scale, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Blocks of a paged cache.  The block table [rows][max_blocks] int32 is the
+ * only record: a block is in use when a row names it (several rows may).  The
+ * table calls read `table` and write `table_out`, which must not overlap it;
+ * the data of blocks moves with csa_blocks_copy, once for each cache (layer)
+ * that shares the table.  Lists are device arrays; ids outside the pool, rows
+ * outside the table and -1 are skipped.
+ * ------------------------------------------------------------------------ */
+enum { CSA_MAX_REGIONS = 16, CSA_MAX_TABLE_BLOCKS = 786432 };
+typedef struct {
+  void* base;         /* device, 16-byte aligned: [num_blocks][block_bytes]     */
+  size_t block_bytes; /* bytes of one block in this region                      */
+} csa_block_region;
+
+/* In every region: block dst[i] becomes a copy of block src[i], i < min(pairs,
+ * count[0]) (count: device int32, NULL: all pairs).  No block may be a
+ * destination twice, nor both a source and a destination (the content of such
+ * blocks is then unspecified).  The per-sequence regions of a cache take
+ * sequence numbers as blocks. */
+csa_status csa_blocks_copy(const csa_block_region* regions, int nregions, int64_t num_blocks,
+                           const int32_t* src, const int32_t* dst, int64_t pairs,
+                           const int32_t* count, void* stream);
+
+/* Row dst[i] becomes a fork of the first tokens[i] tokens (int64) of row
+ * src[i]: it names the source's whole blocks and, where the last block is
+ * partly filled, fresh[i] in its place, with (copy_src[i], copy_dst[i]) the
+ * copy that fills it (-1, -1: none); its remaining entries are -1.  Other rows
+ * are copied.  Of forks with the same dst the last one counts; sources are
+ * read from `table`.  A source outside the table gives an empty row. */
+csa_status csa_blocks_fork(const int32_t* table, int64_t rows, int64_t max_blocks,
+                           const int32_t* src, const int32_t* dst, const int64_t* tokens,
+                           const int32_t* fresh, int forks, int block_tokens, int32_t* table_out,
+                           int32_t* copy_src, int32_t* copy_dst, void* stream);
+
+/* Rows seqs[0 .. nseqs) become -1.  freed [num_blocks]: the blocks that only
+ * those rows named, ascending, then -1; nfreed[0]: how many. */
+csa_status csa_blocks_free(const int32_t* table, int64_t rows, int64_t max_blocks,
+                           int64_t num_blocks, const int32_t* seqs, int nseqs, int32_t* table_out,
+                           int32_t* freed, int32_t* nfreed, void* stream);
+
+/* The blocks in use move to 0 .. live - 1: the j-th one at or above `live` to
+ * the j-th unused one below.  copy_src, copy_dst [num_blocks]: the moves, then
+ * -1; counts [2]: moves, live (counts serves csa_blocks_copy as `count`).
+ * table_out names the new places (entries outside the pool become -1). */
+csa_status csa_blocks_compact(const int32_t* table, int64_t rows, int64_t max_blocks,
+                              int64_t num_blocks, int32_t* table_out, int32_t* copy_src,
+                              int32_t* copy_dst, int32_t* counts, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
