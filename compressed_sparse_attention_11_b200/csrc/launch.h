@@ -197,6 +197,14 @@ cudaError_t launch_attn(const void* q, const void* kv_comp, const int32_t* idx, 
                         const csa_norm_rope* q_nr, void* out, cudaStream_t s,
                         int64_t first = -1);
 
+// Window attention with separate keys and values on the tensor cores (bf16,
+// c = 64 or 128, up to 128 heads per key/value head).
+cudaError_t launch_window_attn_tc(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, int64_t window, int64_t first,
+                                  const float* sink, float scale, int64_t batch, int64_t n_q,
+                                  int64_t n_k, int nh, int nkv, int c, void* out,
+                                  unsigned int* err, cudaStream_t s);
+
 // Grouped output projection: z = grouped o W1^T (bf16 [rows, G dg]), y = z W2^T.
 cudaError_t launch_grouped_out_proj(const void* o, int64_t rows, int nh, int c, int G, int dg,
                                     int d, const void* w1, const void* w2, void* z, void* y,

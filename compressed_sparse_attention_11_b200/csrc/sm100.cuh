@@ -154,6 +154,37 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// 4-D tiled load into shared memory; completes the box's bytes on `bar`.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// 4-D tiled store from shared memory (elements outside the map are not
+// written); part of the thread's bulk group.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y,
+                                             int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit_group() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The thread's bulk groups have read their shared memory (it can be reused).
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// The thread's bulk groups have completed.
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // L2 eviction policy (createpolicy) for data re-read by many CTAs (gathered
 // entries): evict-last.
 __device__ __forceinline__ uint64_t l2_policy_evict_last() {
@@ -441,6 +472,9 @@ __device__ __forceinline__ void tmem_st_wait() {
 bool make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t x, uint64_t y,
                   uint64_t z, uint64_t stride_y_bytes, uint64_t stride_z_bytes, uint32_t box_x,
                   uint32_t box_y);
+// 4-D bf16 map with the 128-byte swizzle: dims, byte strides of dims 1-3, box.
+bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                       const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 inline bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t x, uint64_t y,
                               uint64_t z, uint64_t stride_y_bytes, uint64_t stride_z_bytes,
                               uint32_t box_x, uint32_t box_y) {

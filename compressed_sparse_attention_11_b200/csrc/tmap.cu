@@ -43,6 +43,20 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t x
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                       const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+  std::call_once(g_once, resolve);
+  if (!g_encode) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, bx,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   constexpr int kMaxDev = 64;
   static int counts[kMaxDev] = {};

@@ -26,7 +26,13 @@ extern "C" csa_status csa_window_attn(const void* q, int64_t q_stride, const voi
     API_SUPPORTED(nkv == 1 && n_q == n_k && q_stride == (int64_t)nh * c && k_stride == c,
                   "the shared form needs nkv = 1, n_q = n_k and dense rows");
     API_SUPPORTED(c % 32 == 0 && c <= 512, "attention needs c %% 32 == 0 and c <= 512");
+  } else {
+    API_SUPPORTED(dt == CSA_BF16 && (c == 64 || c == 128),
+                  "window attention with separate values needs bf16 and c = 64 or 128");
+    API_SUPPORTED(nh / nkv <= 128, "window attention needs nh / nkv <= 128");
   }
+  API_SUPPORTED(n_k < ((int64_t)1 << 30) && batch < ((int64_t)1 << 31),
+                "csa_window_attn needs n_k < 2^30");
   if (batch == 0 || n_q == 0) return api_ok();
   API_REQUIRE_PTR(q);
   API_REQUIRE_PTR(k);
@@ -40,5 +46,9 @@ extern "C" csa_status csa_window_attn(const void* q, int64_t q_stride, const voi
                                 n_q, nh, c, 1, dt, nullptr, out, s, first),
                     "csa_window_attn");
   }
-  return set_last_error(CSA_ERR_UNSUPPORTED, "separate values are not supported");
+  unsigned int* flag = device_timeout_flag();
+  if (flag == nullptr) return set_last_error(CSA_ERR_CUDA, "csa_window_attn: no device flag");
+  return api_cuda(launch_window_attn_tc(q, q_stride, k, k_stride, v, v_stride, window, first, sink,
+                                        scale, batch, n_q, n_k, nh, nkv, c, out, flag, s),
+                  "csa_window_attn");
 }

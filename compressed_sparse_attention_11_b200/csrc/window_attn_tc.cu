@@ -1,0 +1,586 @@
+// Causal attention over a sliding window and a few first tokens on the
+// tcgen05 tensor cores, keys and values apart (bf16 in and out, fp32
+// accumulation), head dim C = 64 or 128, heads in groups of g = nh / nkv:
+//   E_t = { u <= t : u > t - W or u < F },
+//   out[t, h] = sum_u e^{l_u} v_u / (e^{sink_h} + sum_u e^{l_u}),  l_u = scale q_th . k_u.
+//
+// Tensor-bound for windows past a few hundred tokens (4 C g flops a visible
+// pair against 2 C / g bytes).  A query tile is 128 rows: the g heads of one
+// key/value head times TT = 128 / g consecutive tokens, so the heads of a
+// group share every key tile and a tile's band of keys is W + TT - 1 wide,
+// not W + 127.  A CTA (one per SM, persistent) takes pairs of neighbouring
+// query tiles; while the softmax of one runs, the products of the other do:
+//   S_q = Q_q K^T (M = 128 rows, N = 128 keys), O_q += P_q V (N = C dims).
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (C each); P takes its
+// S's first 64 columns (bf16) and is the A operand of P.V from there.
+//
+// Key order: with F > 0 and the pair's window starting past F, the tile
+// list starts with the F first tokens (rounded up to 8 rows) and goes on with
+// the window without a gap, the mixed tile being fetched in 8-row boxes, so
+// a few first tokens do not cost a tile of their own.  Virtual column
+// v < F8 is token v (visible if v < F), v >= F8 token klo + v - F8.
+//
+// Softmax: one thread per row (two warpgroups, one per query tile), running
+// maximum that moves only past 2^8 (the row of O is then rescaled in tensor
+// memory), weights rounded to bf16 for the second product while the sum takes
+// them unrounded.
+//
+// A value row that is not finite where a query's mask hides it would still
+// reach that query through 0 x inf in the second product.  The epilogue sees
+// that as an output that is not finite and recomputes the row from global
+// memory over its visible keys alone; no other row pays for it.
+#include "api_check.h"
+#include "common.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+#include "tc_attn_util.cuh"
+
+namespace csa {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kSlab = kRows * 128;  // 16 KB: 128 rows x 64 dims
+constexpr int kStages = 2;
+constexpr int kSoftWarps = 8;  // two warpgroups
+constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + 1;
+constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr float kRescaleLog2 = 8.f;
+
+struct WinArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const float* sink;
+  __nv_bfloat16* out;
+  unsigned int* err;
+  int64_t works;
+  int nq, nk, window, first, nh, nkv, group, tt, pairs;
+  float qs;  // |scale| log2(e), never 0
+  int neg;   // the scale is negative
+};
+
+template <int C>
+struct Cfg {
+  static constexpr int kSlabs = C / 64;
+  static constexpr int kTileBytes = kSlabs * kSlab;
+  static constexpr int off_q = 0;
+  static constexpr int off_k = off_q + 2 * kTileBytes;
+  static constexpr int off_v = off_k + kStages * kTileBytes;
+  static constexpr int off_e = off_v + kStages * kTileBytes;  // 2 x 16 KB epilogue staging
+  static constexpr int off_bar = off_e + 2 * kSlab;
+  static constexpr int smem = off_bar + 512 + 1024;
+  static constexpr uint32_t col_s = 0, col_o = 256;
+};
+
+struct __align__(8) WinBars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t wg[2];  // bounded barrier of the four warps of a warpgroup
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t odd[2];  // a row of the query tile has an output that is not finite
+};
+
+// One pair of query tiles and its list of key tiles.
+struct Job {
+  int b, h, i0;        // batch, key/value head, first query
+  int t0, t1;          // positions of the pair's first and last query
+  int klo, f8, tiles;  // see the head comment
+  __device__ int base(int j) const { return klo - f8 + j * kKeys; }  // token of column 0 (window part)
+};
+__device__ __forceinline__ Job job_of(const WinArgs& a, int64_t w) {
+  Job j;
+  const int pair = (int)(w % a.pairs);
+  const int64_t r = w / a.pairs;
+  j.h = (int)(r % a.nkv);
+  j.b = (int)(r / a.nkv);
+  j.i0 = pair * 2 * a.tt;
+  j.t0 = a.nk - a.nq + j.i0;
+  j.t1 = a.nk - a.nq + min(a.nq, j.i0 + 2 * a.tt) - 1;
+  j.klo = max(0, j.t0 - a.window + 1);
+  if (a.first >= j.klo) j.klo = 0;
+  j.f8 = j.klo > 0 ? (a.first + 7) & ~7 : 0;
+  j.tiles = (j.f8 + j.t1 - j.klo + kKeys) / kKeys;
+  return j;
+}
+// First columns of tile tj that are visible as first tokens, whatever the row.
+__device__ __forceinline__ int first_cols(const WinArgs& a, const Job& j, int tj) {
+  return j.f8 > 0 ? a.first - tj * kKeys : a.first - j.base(tj);
+}
+__device__ __forceinline__ bool active(const WinArgs& a, const Job& j, int q) {
+  return j.i0 + q * a.tt < a.nq;
+}
+// Whether a row of query tile q sees a key of tile tj.
+__device__ __forceinline__ bool needs(const WinArgs& a, const Job& j, int q, int tj) {
+  if (!active(a, j, q)) return false;
+  const int ta = j.t0 + q * a.tt, tb = min(ta + a.tt - 1, j.t1), base = j.base(tj);
+  if (base > tb) return false;
+  return (ta - a.window + 1 - base < kKeys && (tj + 1) * kKeys > j.f8) || first_cols(a, j, tj) > 0;
+}
+
+// (q, k) of a row and key in fp32, the lanes of the warp sharing the dims.
+template <int C>
+__device__ __noinline__ void exact_row(const WinArgs& a, const Job& j, int i, int head, float m,
+                                       float inv, __nv_bfloat16* out) {
+  const int lane = threadIdx.x & 31;
+  constexpr int E = C / 32;
+  const __nv_bfloat16* q = a.q + ((int64_t)j.b * a.nq + i) * a.q_stride + (int64_t)head * C;
+  float qv[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qv[e] = __bfloat162float(q[lane + 32 * e]);
+    acc[e] = 0.f;
+  }
+  const int t = a.nk - a.nq + i;
+  for (int u = 0; u <= t; ++u) {
+    if (u >= a.first && u <= t - a.window) u = t - a.window + 1;  // on to the window
+    const int64_t row = (int64_t)j.b * a.nk + u;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      s = fmaf(qv[e], __bfloat162float(a.k[row * a.k_stride + (int64_t)j.h * C + lane + 32 * e]), s);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const float p = ex2(fmaf(a.neg ? -s : s, a.qs, -m));
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      acc[e] = fmaf(p, __bfloat162float(a.v[row * a.v_stride + (int64_t)j.h * C + lane + 32 * e]), acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+}
+
+template <int C>
+__global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k8,
+    const __grid_constant__ CUtensorMap tm_v8, const __grid_constant__ CUtensorMap tm_o,
+    const __grid_constant__ WinArgs a) {
+  using F = Cfg<C>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  WinBars* bar = reinterpret_cast<WinBars*>(smem + F::off_bar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned int* err = a.err;
+  if (flag_value(err) != 0) return;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->q_full[i], 1);
+      mbar_init(&bar->q_free[i], 1);
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->o_full[i], 1);
+      mbar_init(&bar->o_free[i], 4);
+      mbar_init(&bar->wg[i], 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_free[i], 1);
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_free[i], 1);
+    }
+    mbar_init(&bar->drain, 1);
+    bar->odd[0] = bar->odd[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bar->tmem_base, 512);
+    tmem_relinquish();
+  }
+  // rows of the query tiles that no token fills stay zero
+  for (int i = threadIdx.x; i < 2 * F::kTileBytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(smem + F::off_q)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+
+  if (warp == kTmaWarp) {
+    // ================================ TMA producer ================================
+    int n = 0;               // key tiles issued
+    int nq[2] = {0, 0};      // query tiles issued
+    bool ok = true;
+    for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+      const Job jb = job_of(a, w);
+      auto load_q = [&](int q) {
+        if (!active(a, jb, q)) return;
+        if (nq[q] > 0 && !mbar_wait(&bar->q_free[q], (uint32_t)((nq[q] - 1) & 1), err)) {
+          ok = false;
+          return;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar->q_full[q], (uint32_t)(a.tt * a.group * 128 * F::kSlabs));
+          for (int s = 0; s < F::kSlabs; ++s)
+            tma_load_4d(smem + F::off_q + q * F::kTileBytes + s * kSlab, &tm_q, &bar->q_full[q],
+                        s * 64, jb.h * a.group, jb.i0 + q * a.tt, jb.b);
+        }
+        __syncwarp();
+        ++nq[q];
+      };
+      auto load_tile = [&](int tj, int off, uint64_t* full, const CUtensorMap* m, const CUtensorMap* m8) {
+        uint8_t* dst = smem + off;
+        if (lane == 0) mbar_arrive_expect_tx(full, F::kTileBytes);
+        __syncwarp();
+        const int v0 = tj * kKeys;
+        if (v0 < jb.f8 && v0 + kKeys > jb.f8) {  // first tokens, then the window: 8-row boxes
+          if (lane < 16) {
+            const int v = v0 + 8 * lane;
+            const int u = v < jb.f8 ? v : jb.klo + v - jb.f8;
+            for (int s = 0; s < F::kSlabs; ++s)
+              tma_load_4d(dst + s * kSlab + lane * 1024, m8, full, s * 64, jb.h, u, jb.b);
+          }
+        } else if (lane == 0) {
+          const int u = v0 < jb.f8 ? v0 : jb.base(tj);
+          for (int s = 0; s < F::kSlabs; ++s)
+            tma_load_4d(dst + s * kSlab, m, full, s * 64, jb.h, u, jb.b);
+        }
+        __syncwarp();
+      };
+      load_q(0);
+      for (int tj = 0; tj < jb.tiles && ok; ++tj, ++n) {
+        const int st = n % kStages;
+        const uint32_t ph = (uint32_t)((n / kStages - 1) & 1);
+        if (n >= kStages && !(ok = mbar_wait(&bar->k_free[st], ph, err))) break;
+        load_tile(tj, F::off_k + st * F::kTileBytes, &bar->k_full[st], &tm_k, &tm_k8);
+        if (tj == 0) {
+          load_q(1);
+          if (!ok) {  // the values of this tile will not come: it counts as not issued
+            mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err, false);
+            break;
+          }
+        }
+        if (n >= kStages && !(ok = mbar_wait(&bar->v_free[st], ph, err))) {
+          mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err, false);
+          break;
+        }
+        load_tile(tj, F::off_v + st * F::kTileBytes, &bar->v_full[st], &tm_v, &tm_v8);
+      }
+    }
+    // every load has landed before the CTA ends
+    for (int i = n > kStages ? n - kStages : 0; i < n; ++i) {
+      mbar_wait(&bar->k_full[i % kStages], (uint32_t)((i / kStages) & 1), err, false);
+      mbar_wait(&bar->v_full[i % kStages], (uint32_t)((i / kStages) & 1), err, false);
+    }
+    for (int q = 0; q < 2; ++q)
+      if (nq[q] > 0) mbar_wait(&bar->q_full[q], (uint32_t)((nq[q] - 1) & 1), err, false);
+  } else if (warp == kMmaWarp) {
+    // ================================ MMA issuer ==================================
+    constexpr uint32_t kIdQK = idesc_bf16(kRows, kKeys, 0, 0);
+    constexpr uint32_t kIdPV = idesc_bf16(kRows, C, 0, 1);
+    const uint32_t q0 = smem_u32(smem + F::off_q), k0 = smem_u32(smem + F::off_k),
+                   v0 = smem_u32(smem + F::off_v);
+    int n = 0;                    // key tiles of all jobs
+    int v_next = 0;               // next value tile to be freed
+    int pend[2] = {-1, -1};       // key tile whose P.V is still to be issued
+    bool pend_first[2], pend_last[2];
+    int pvs[2] = {0, 0}, jobs[2] = {0, 0}, done[2] = {0, 0};  // P.V issued, query tiles begun / finished
+    bool ok = true;
+    auto issue_pv = [&](int q) -> bool {
+      const int st = pend[q] % kStages;
+      if (!mbar_wait(&bar->p_full[q], (uint32_t)(pvs[q] & 1), err)) return false;
+      if (!mbar_wait(&bar->v_full[st], (uint32_t)((pend[q] / kStages) & 1), err)) return false;
+      // the first P.V of a query tile overwrites O: the epilogue before has read it
+      if (pend_first[q] && done[q] > 0 &&
+          !mbar_wait(&bar->o_free[q], (uint32_t)((done[q] - 1) & 1), err))
+        return false;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_bf16_ts(tmem + F::col_o + q * C, tmem + F::col_s + q * kKeys + kk * 8,
+                      desc_sw128_mn(v0 + st * F::kTileBytes + kk * 2048, kSlab, 1024), kIdPV,
+                      (pend_first[q] && kk == 0) ? 0u : 1u);
+        if (pend_last[q]) mma_commit(&bar->o_full[q]);
+      }
+      __syncwarp();
+      if (pend_last[q]) ++done[q];
+      ++pvs[q];
+      pend[q] = -1;
+      return true;
+    };
+    // value tiles that no P.V to come reads
+    auto free_v = [&](int upto) {
+      while (v_next < upto && v_next != pend[0] && v_next != pend[1]) {
+        if (lane == 0) mma_commit(&bar->v_free[v_next % kStages]);
+        ++v_next;
+      }
+      __syncwarp();
+    };
+    for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+      const Job jb = job_of(a, w);
+      bool first[2] = {true, true};
+      int last[2];
+      for (int q = 0; q < 2; ++q) {
+        last[q] = jb.tiles - 1;
+        while (last[q] >= 0 && !needs(a, jb, q, last[q])) --last[q];
+      }
+      for (int tj = 0; tj < jb.tiles && ok; ++tj, ++n) {
+        const int st = n % kStages;
+        bool have_k = false;
+        for (int q = 0; q < 2 && ok; ++q) {
+          // the value ring never waits for a query tile that has no more work
+          if (pend[q] >= 0) {
+            if (!(ok = issue_pv(q))) break;
+            free_v(n);
+          }
+          if (!needs(a, jb, q, tj)) continue;
+          if (first[q] && !(ok = mbar_wait(&bar->q_full[q], (uint32_t)(jobs[q] & 1), err))) break;
+          if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err))) break;
+          have_k = true;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk)
+              mma_bf16(tmem + F::col_s + q * kKeys,
+                       desc_sw128(q0 + q * F::kTileBytes + (kk >> 2) * kSlab + (kk & 3) * 32),
+                       desc_sw128(k0 + st * F::kTileBytes + (kk >> 2) * kSlab + (kk & 3) * 32),
+                       kIdQK, kk != 0 ? 1u : 0u);
+            mma_commit(&bar->s_full[q]);
+            if (tj == last[q]) mma_commit(&bar->q_free[q]);
+          }
+          __syncwarp();
+          pend[q] = n;
+          pend_first[q] = first[q];
+          pend_last[q] = tj == last[q];
+          if (first[q]) ++jobs[q];
+          first[q] = false;
+        }
+        if (!ok) break;
+        // a tile that no row needs was loaded all the same: wait for it, then free it
+        if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err) &&
+                              mbar_wait(&bar->v_full[st], (uint32_t)((n / kStages) & 1), err)))
+          break;
+        if (lane == 0) mma_commit(&bar->k_free[st]);
+        __syncwarp();
+        free_v(n);
+      }
+    }
+    for (int q = 0; q < 2 && ok; ++q)
+      if (pend[q] >= 0) ok = issue_pv(q);
+    if (lane == 0) mma_commit(&bar->drain);
+    __syncwarp();
+    mbar_wait(&bar->drain, 0, err, false);
+  } else {
+    // ============================ softmax and epilogue ============================
+    const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_addr + F::col_s + q * kKeys;
+    const uint32_t o_addr = tmem + lane_addr + F::col_o + q * C;
+    const int tl = row / a.group, hl = row - tl * a.group;  // token and head of the row
+    uint8_t* stage = smem + F::off_e + q * kSlab;
+    int steps = 0, jobs = 0;
+    uint32_t wg_phase = 0;
+    bool ok = true;
+    for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+      const Job jb = job_of(a, w);
+      if (!active(a, jb, q)) continue;
+      const int ta = jb.t0 + q * a.tt, t = ta + tl;
+      const int tb = min(ta + a.tt - 1, jb.t1);
+      float m = kNegInf, l = 0.f;
+      int t_first = -1;  // the first tile that the query tile needs (O is not yet written there)
+      for (int tj = 0; tj < jb.tiles; ++tj) {
+        if (!needs(a, jb, q, tj)) continue;
+        if (t_first < 0) t_first = tj;
+        if (!(ok = mbar_wait(&bar->s_full[q], (uint32_t)(steps & 1), err))) break;
+        ++steps;
+        tc_fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c)
+          tmem_ld32(s_addr + c * 32, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+        tmem_ld_wait();
+        if (a.neg) {
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) s[i] = -s[i];
+        }
+        const int base = jb.base(tj), fc = first_cols(a, jb, tj);
+        if (base + kKeys - 1 > ta || tb - a.window + 1 > base) {  // some row hides a key
+          const int hi = t - base, lo = t - a.window + 1 - base;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (!(i <= hi && (i >= lo || i < fc))) s[i] = kNegInf;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.qs;
+        const bool grow = top > m + kRescaleLog2;
+        if (__any_sync(0xffffffffu, grow)) {
+          // O is complete up to the tile before: its P.V was issued before this S
+          const float mn = grow ? top : m;
+          const float f = grow ? ex2(m - mn) : 1.f;  // 0 for the first keys of a row
+          if (tj != t_first) {
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < C / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(o_addr + c * 32, o);
+            }
+            tmem_st_wait();
+          }
+          m = mn;
+        }
+        const float mr = m == kNegInf ? 0.f : m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float p0 = ex2(fmaf(s[64 * c + i], a.qs, -mr));
+            const float p1 = ex2(fmaf(s[64 * c + i + 1], a.qs, -mr));
+            ls[i & 3] += p0;
+            ls[(i & 3) + 1] += p1;
+            pk[i >> 1] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(s_addr + c * 32, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->p_full[q]);
+      }
+      if (!ok) break;
+      // ---- out = O / (sum + 2^(sink - m)) ------------------------------------------
+      if (!(ok = mbar_wait(&bar->o_full[q], (uint32_t)(jobs & 1), err))) break;
+      ++jobs;
+      tc_fence_after();
+      const int head = jb.h * a.group + hl;
+      const int i = jb.i0 + q * a.tt + tl;
+      const bool real = tl < a.tt && i < a.nq;
+      const float mr = m == kNegInf ? 0.f : m;
+      const float z = real && a.sink != nullptr ? a.sink[head] * kLog2e : kNegInf;
+      const float inv = 1.f / (l + ex2(z - mr));
+      bool odd = false;  // an output that is not finite
+#pragma unroll 1
+      for (int sl = 0; sl < F::kSlabs; ++sl) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + sl * 64 + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float x = __uint_as_float(o[e]) * inv, y = __uint_as_float(o[e + 1]) * inv;
+            odd |= !(fabsf(x) <= 3.4028234664e38f) || !(fabsf(y) <= 3.4028234664e38f);
+            pk[16 * c + (e >> 1)] = pack_bf16x2(x, y);
+          }
+        }
+        if (sl == F::kSlabs - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->o_free[q]);
+        }
+        // the slab before has left the staging buffer (its store was issued by
+        // the warpgroup's first thread)
+        if (row == 0) bulk_wait_read();
+        if (!(ok = group_sync(&bar->wg[q], wg_phase, err))) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) * 16)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        if (odd && real) bar->odd[q] = 1;
+        fence_proxy_async();
+        if (!(ok = group_sync(&bar->wg[q], wg_phase, err))) break;
+        if (row == 0) {
+          tma_store_4d(&tm_o, stage, sl * 64, jb.h * a.group, jb.i0 + q * a.tt, jb.b);
+          bulk_commit_group();
+        }
+      }
+      if (!ok) break;
+      if (bar->odd[q] == 0) continue;
+      // (rare) such rows again, key by key, once the warpgroup's stores are done
+      if (row == 0) bulk_wait_all();
+      if (!(ok = group_sync(&bar->wg[q], wg_phase, err))) break;
+      if (row == 0) bar->odd[q] = 0;
+      unsigned todo = __ballot_sync(0xffffffffu, odd && real);
+      while (todo) {
+        const int r = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int ri = __shfl_sync(0xffffffffu, i, r), rh = __shfl_sync(0xffffffffu, head, r);
+        const float rm = __shfl_sync(0xffffffffu, mr, r), rinv = __shfl_sync(0xffffffffu, inv, r);
+        exact_row<C>(a, jb, ri, rh, rm, rinv,
+                     a.out + (((int64_t)jb.b * a.nq + ri) * a.nh + rh) * C);
+      }
+    }
+    if (row == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int C>
+cudaError_t launch_c(WinArgs a, int64_t batch, cudaStream_t s) {
+  using F = Cfg<C>;
+  CUtensorMap mq, mk, mv, mk8, mv8, mo;
+  const uint64_t nq = a.nq, nk = a.nk, nh = a.nh, nkv = a.nkv, B = batch;
+  const uint64_t dq[4] = {C, nh, nq, B}, dk[4] = {C, nkv, nk, B};
+  const uint64_t qs = 2 * (uint64_t)a.q_stride, ks = 2 * (uint64_t)a.k_stride,
+                 vs = 2 * (uint64_t)a.v_stride, os = 2 * nh * C;
+  const uint32_t bq[4] = {64, (uint32_t)a.group, (uint32_t)a.tt, 1}, bk[4] = {64, 1, kKeys, 1},
+                 b8[4] = {64, 1, 8, 1};
+  if (!make_tmap_bf16_4d(&mq, a.q, dq, {2 * C, qs, qs * nq}, bq) ||
+      !make_tmap_bf16_4d(&mo, a.out, dq, {2 * C, os, os * nq}, bq) ||
+      !make_tmap_bf16_4d(&mk, a.k, dk, {2 * C, ks, ks * nk}, bk) ||
+      !make_tmap_bf16_4d(&mv, a.v, dk, {2 * C, vs, vs * nk}, bk) ||
+      !make_tmap_bf16_4d(&mk8, a.k, dk, {2 * C, ks, ks * nk}, b8) ||
+      !make_tmap_bf16_4d(&mv8, a.v, dk, {2 * C, vs, vs * nk}, b8))
+    return cudaErrorInvalidValue;
+  auto kern = window_attn_kernel<C>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<int64_t>(a.works, sm_count());
+  kern<<<grid, kThreads, F::smem, s>>>(mq, mk, mv, mk8, mv8, mo, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_attn_tc(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, int64_t window, int64_t first,
+                                  const float* sink, float scale, int64_t batch, int64_t n_q,
+                                  int64_t n_k, int nh, int nkv, int c, void* out,
+                                  unsigned int* err, cudaStream_t s) {
+  WinArgs a;
+  a.q = (const __nv_bfloat16*)q;
+  a.k = (const __nv_bfloat16*)k;
+  a.v = (const __nv_bfloat16*)v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.sink = sink;
+  a.out = (__nv_bfloat16*)out;
+  a.err = err;
+  a.nq = (int)n_q;
+  a.nk = (int)n_k;
+  a.window = (int)std::min(window, n_k);
+  a.first = (int)std::min(first, n_k);
+  a.nh = nh;
+  a.nkv = nkv;
+  a.group = nh / nkv;
+  a.tt = kRows / a.group;
+  a.pairs = (int)((n_q + 2 * a.tt - 1) / (2 * a.tt));
+  a.works = (int64_t)a.pairs * nkv * batch;
+  a.neg = scale < 0.f;
+  // a scale of 0 weighs every visible key alike, as does this
+  a.qs = std::max(std::abs(scale) * kLog2e, 1e-30f);
+  return c == 128 ? launch_c<128>(a, batch, s) : launch_c<64>(a, batch, s);
+}
+
+}  // namespace csa
