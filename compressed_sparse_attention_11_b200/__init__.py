@@ -419,46 +419,56 @@ def csa_grouped_out_proj(o, w1, w2, ws: Optional[torch.Tensor] = None,
 
 # --------------------------------------- head norms, window, 4-bit cache, blocks ---
 
-class _On:
-    """Makes a tensor's device the current one around a call that asks for the device."""
+# These calls take microseconds on the GPU, so their marshalling is kept short:
+# one device query per tensor, a single strides pass for dense tensors, and the
+# library's functions looked up once.
 
-    def __init__(self, t: torch.Tensor):
-        self.guard = None if t.device.index == torch.cuda.current_device() else \
-            torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, dev: int, *args):
+    """fn(*args, current stream of device ``dev``) with that device current."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
-def _dev_ptr(t: Optional[torch.Tensor], like: torch.Tensor, dtype, name: str, numel=None):
-    """Pointer of a dense tensor of the given type on ``like``'s device (None: NULL)."""
+def _device(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return dev
+
+
+def _dense(t: Optional[torch.Tensor], dev: int, dtype, name: str, numel: int = -1):
+    """Pointer of a dense tensor of the given type on device ``dev`` (None: NULL)."""
     if t is None:
         return None
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must live on {like.device}")
-    if numel is not None and t.numel() != numel:
+    if t.get_device() != dev:
+        _device(t)
+        raise ValueError(f"{name} must live on cuda:{dev}")
+    if numel >= 0 and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _tokens_view(x: torch.Tensor, name: str):
     """(tokens, stride) of x [..., heads, c] whose heads are dense and whose
     leading dims step by one token stride (elements)."""
-    if not x.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    shape, strides = x.shape, x.stride()
+    shape = x.shape
     heads, c = shape[-2], shape[-1]
+    if x.is_contiguous():
+        return (x.numel() // (heads * c) if heads and c else 0), heads * c
+    strides = x.stride()
     if (c > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != c):
         raise ValueError(f"the heads of {name} must be dense")
     tokens, step = 1, 0
-    for size, st in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+    for size, st in zip(shape[-3::-1], strides[-3::-1]):
         if size == 1:
             continue
         if tokens == 1:
@@ -466,8 +476,6 @@ def _tokens_view(x: torch.Tensor, name: str):
         elif st != step * tokens:
             raise ValueError(f"the tokens of {name} must step by one stride")
         tokens *= size
-    if 0 in shape:
-        tokens = 0
     return tokens, (step if tokens > 1 else heads * c)
 
 
@@ -484,47 +492,55 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    c, dt = ref.shape[-1], _dt(ref)
-    args, tokens = [], None
-    for x, out, gamma, name in ((q, q_out, q_gamma, "q"), (k, k_out, k_gamma, "k")):
-        if x is None:
-            args.append((None, c, None, c, 0, None))
-            continue
-        if x.dtype != ref.dtype or x.device != ref.device or x.shape[-1] != c:
-            raise ValueError("q and k must have one dtype, device and head dim")
-        heads = x.shape[-2]
-        n, step = _tokens_view(x, name)
-        if tokens is not None and n != tokens:
-            raise ValueError("q and k must have the same tokens")
+    dev, dt, c, dtype = _device(ref), _dt(ref), ref.shape[-1], ref.dtype
+    qp = kp = qop = kop = qg = kg = None
+    qs = ks = qos = kos = nh = nkv = 0
+    tokens = per_head = None
+    if q is not None:
+        nh = q.shape[-2]
+        tokens, qs = _tokens_view(q, "q")
+        if q_out is None:
+            q_out, qos = torch.empty(q.shape, dtype=dtype, device=q.device), nh * c
+        else:
+            if q_out.shape != q.shape or q_out.dtype != dtype or q_out.get_device() != dev:
+                raise ValueError("q_out must be like q")
+            qos = _tokens_view(q_out, "q_out")[1]
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+        if q_gamma is not None:
+            per_head = q_gamma.dim()
+            qg = _dense(q_gamma, dev, torch.float32, "q_gamma", c if per_head == 1 else nh * c)
+    if k is not None:
+        nkv = k.shape[-2]
+        n, ks = _tokens_view(k, "k")
+        if n != (n if tokens is None else tokens) or k.dtype != dtype or k.get_device() != dev \
+                or k.shape[-1] != c:
+            raise ValueError("q and k must have the same tokens, head dim, dtype and device")
         tokens = n
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-            raise ValueError(f"{name}_out must be like {name}")
-        gp = None
-        if gamma is not None:
-            if tuple(gamma.shape) not in ((c,), (heads, c)):
-                raise ValueError(f"{name}_gamma must be [c] or [heads, c]")
-            gp = _dev_ptr(gamma, ref, torch.float32, f"{name}_gamma")
-        args.append((x.data_ptr(), step, out, _tokens_view(out, f"{name}_out")[1], heads, gp))
-    dims = {g.dim() for x, g in ((q, q_gamma), (k, k_gamma)) if x is not None and g is not None}
-    if len(dims) == 2:
-        raise ValueError("q_gamma and k_gamma must both be [c] or both be [heads, c]")
+        if k_out is None:
+            k_out, kos = torch.empty(k.shape, dtype=dtype, device=k.device), nkv * c
+        else:
+            if k_out.shape != k.shape or k_out.dtype != dtype or k_out.get_device() != dev:
+                raise ValueError("k_out must be like k")
+            kos = _tokens_view(k_out, "k_out")[1]
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        if k_gamma is not None:
+            if per_head not in (None, k_gamma.dim()):
+                raise ValueError("q_gamma and k_gamma must both be [c] or both be [heads, c]")
+            per_head = k_gamma.dim()
+            kg = _dense(k_gamma, dev, torch.float32, "k_gamma", c if per_head == 1 else nkv * c)
+    p = QkRope(qg, kg, 1 if per_head == 2 else 0, eps, rope_dims, rope_base, 1 if halves else 0)
     if sections is None:
-        sections = (rope_dims // 2,)
-    if not 1 <= len(sections) <= 4:
-        raise ValueError("1 to 4 sections")
-    pp = None
-    if rope_dims > 0:
-        pp = _dev_ptr(pos, ref, torch.int64, "pos", len(sections) * tokens)
-    (qp, qs, qo, qos, nh, qg), (kp, ks, ko, kos, nkv, kg) = args
-    p = QkRope(qg, kg, 1 if dims == {2} else 0, float(eps), int(rope_dims), float(rope_base),
-               1 if halves else 0, len(sections), (ctypes.c_int32 * 4)(*sections))
-    with _On(ref):
-        _check(lib().csa_qk_norm_rope(qp, qs, kp, ks, tokens, nh, nkv, c, pp, ctypes.byref(p), dt,
-                                      None if qo is None else qo.data_ptr(), qos,
-                                      None if ko is None else ko.data_ptr(), kos, _stream(ref)))
-    return qo, ko
+        p.axes, p.sections[0] = 1, rope_dims // 2
+    else:
+        p.axes = len(sections)
+        if not 1 <= p.axes <= 4:
+            raise ValueError("1 to 4 sections")
+        for i, n in enumerate(sections):
+            p.sections[i] = n
+    pp = _dense(pos, dev, torch.int64, "pos", p.axes * tokens) if rope_dims else None
+    _call(lib().csa_qk_norm_rope, dev, qp, qs, kp, ks, tokens, nh, nkv, c, pp, ctypes.byref(p), dt,
+          qop, qos, kop, kos)
+    return q_out if q is not None else None, k_out if k is not None else None
 
 
 def csa_window_attn(q, k, v, window: int, first: int = 0, sink=None, scale: float = 1.0,
@@ -537,24 +553,24 @@ def csa_window_attn(q, k, v, window: int, first: int = 0, sink=None, scale: floa
         k = k.unsqueeze(2)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, n_q, nh, c] and k [B, n_k, nkv, c]")
+    dev, dt, dtype = _device(q), _dt(q), q.dtype
     B, nq, nh, c = q.shape
-    nk, nkv = k.shape[1], k.shape[2]
-    for x, name in ((k, "k"), (v, "v")):
-        if x is not None and (tuple(x.shape) != (B, nk, nkv, c) or x.dtype != q.dtype
-                              or x.device != q.device):
-            raise ValueError(f"{name} must be [B, n_k, nkv, c] of q's dtype and device")
+    _, nk, nkv, ck = k.shape
+    if k.shape[0] != B or ck != c or k.dtype != dtype or k.get_device() != dev:
+        raise ValueError("k must be [B, n_k, nkv, c] of q's dtype and device")
+    vp, vs = None, 0
+    if v is not None:
+        if v.shape != k.shape or v.dtype != dtype or v.get_device() != dev:
+            raise ValueError("v must be like k")
+        vp, vs = v.data_ptr(), _tokens_view(v, "v")[1]
     if out is None:
-        out = torch.empty((B, nq, nh, c), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (B, nq, nh, c) or out.dtype != q.dtype or out.device != q.device:
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    elif out.shape != q.shape:
         raise ValueError("out must be like q")
-    qs, ks = _tokens_view(q, "q")[1], _tokens_view(k, "k")[1]
-    vs = 0 if v is None else _tokens_view(v, "v")[1]
-    sp = _dev_ptr(sink, q, torch.float32, "sink", nh)
-    with _On(q):
-        _check(lib().csa_window_attn(q.data_ptr(), qs, k.data_ptr(), ks,
-                                     None if v is None else v.data_ptr(), vs, int(window),
-                                     int(first), sp, float(scale), B, nq, nk, nh, nkv, c, _dt(q),
-                                     _ptr(out), _stream(q)))
+    _call(lib().csa_window_attn, dev, q.data_ptr(), _tokens_view(q, "q")[1], k.data_ptr(),
+          _tokens_view(k, "k")[1], vp, vs, window, first,
+          _dense(sink, dev, torch.float32, "sink", nh), scale, B, nq, nk, nh, nkv, c, dt,
+          _dense(out, dev, dtype, "out"))
     return out
 
 
@@ -573,48 +589,43 @@ def csa_kv4_cache(num_blocks: int, nkv: int, c: int, block_tokens: int = 128,
                        device=device)
 
 
-def _kv4_desc(cache: torch.Tensor, block_table: torch.Tensor) -> Kv4Desc:
-    if cache.dtype != torch.uint8 or cache.dim() != 4:
-        raise ValueError("cache must be a uint8 [num_blocks, nkv, block_tokens / 16, bytes] tensor")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be an int32 [batch, max_blocks] tensor")
+def _kv4_desc(cache: torch.Tensor, block_table: torch.Tensor):
+    """(device, descriptor, nkv, c) of a cache and its block table."""
+    if cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("cache must be a uint8 [num_blocks, nkv, block_tokens / 16, bytes] tensor "
+                         "and block_table an int32 [batch, max_blocks] tensor")
+    dev = _device(cache)
     nb, nkv, tiles, by = cache.shape
-    return Kv4Desc(_ptr(cache), _dev_ptr(block_table, cache, torch.int32, "block_table"),
-                   block_table.shape[0], block_table.shape[1], nb, nkv, (by - 32) // 18,
-                   16 * tiles)
-
-
-def _kv4_pos(d: Kv4Desc, cache, pos, count):
-    return (_dev_ptr(pos, cache, torch.int64, "pos", d.batch),
-            _dev_ptr(count, cache, torch.int32, "count", d.batch))
+    c = (by - 32) // 18
+    return dev, Kv4Desc(_dense(cache, dev, torch.uint8, "cache"),
+                        _dense(block_table, dev, torch.int32, "block_table"), *block_table.shape,
+                        nb, nkv, c, 16 * tiles), nkv, c
 
 
 def csa_kv4_store(cache, block_table, pos, k, v, count: Optional[torch.Tensor] = None):
     """Stores k and v [B, n, nkv, c] (bf16 or fp32, views with one token
     stride) in 4 bits at positions pos[b] + i; count: int32 [B] rows to store."""
-    d = _kv4_desc(cache, block_table)
-    for x, name in ((k, "k"), (v, "v")):
-        if x.dim() != 4 or x.shape[0] != d.batch or tuple(x.shape[2:]) != (d.nkv, d.c) \
-                or x.shape != k.shape or x.dtype != k.dtype or x.device != cache.device:
-            raise ValueError(f"{name} must be [batch, n, nkv, c] on the cache's device")
-    pp, cp = _kv4_pos(d, cache, pos, count)
-    ks, vs = _tokens_view(k, "k")[1], _tokens_view(v, "v")[1]
-    with _On(cache):
-        _check(lib().csa_kv4_store(ctypes.byref(d), pp, k.shape[1], cp, k.data_ptr(), ks,
-                                   v.data_ptr(), vs, _dt(k), _stream(cache)))
+    dev, d, nkv, c = _kv4_desc(cache, block_table)
+    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or k.get_device() != dev \
+            or v.get_device() != dev or k.shape[2] != nkv or k.shape[3] != c \
+            or k.shape[0] != block_table.shape[0]:
+        raise ValueError("k and v must be [batch, n, nkv, c] on the cache's device")
+    B, n = k.shape[0], k.shape[1]
+    _call(lib().csa_kv4_store, dev, ctypes.byref(d), _dense(pos, dev, torch.int64, "pos", B), n,
+          _dense(count, dev, torch.int32, "count", B), k.data_ptr(), _tokens_view(k, "k")[1],
+          v.data_ptr(), _tokens_view(v, "v")[1], _dt(k))
 
 
 def csa_kv4_fetch(cache, block_table, pos, n: int, count: Optional[torch.Tensor] = None,
                   dtype=torch.bfloat16):
     """The stored rows of positions pos[b] .. pos[b] + n - 1 as k, v [B, n, nkv, c]
     (zeros from row count[b] on and where the block is absent)."""
-    d = _kv4_desc(cache, block_table)
-    pp, cp = _kv4_pos(d, cache, pos, count)
-    k = torch.empty((d.batch, n, d.nkv, d.c), dtype=dtype, device=cache.device)
-    v = torch.empty_like(k)
-    with _On(cache):
-        _check(lib().csa_kv4_fetch(ctypes.byref(d), pp, n, cp, _dt(k), _ptr(k), _ptr(v),
-                                   _stream(cache)))
+    dev, d, nkv, c = _kv4_desc(cache, block_table)
+    B = block_table.shape[0]
+    k = torch.empty((B, n, nkv, c), dtype=dtype, device=cache.device)
+    v = torch.empty((B, n, nkv, c), dtype=dtype, device=cache.device)
+    _call(lib().csa_kv4_fetch, dev, ctypes.byref(d), _dense(pos, dev, torch.int64, "pos", B), n,
+          _dense(count, dev, torch.int32, "count", B), _dt(k), k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -628,24 +639,26 @@ def csa_kv4_decode_attn(q, cache, block_table, pos, scale: float, window: int = 
     """Attention of one query token per sequence, q [B, nh, c] bf16 at position
     pos[b] (already stored), over the 4-bit cache: every token, or with
     ``window`` the last ``window`` and the first ``first`` ones."""
-    d = _kv4_desc(cache, block_table)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != d.batch or q.shape[2] != d.c \
-            or q.device != cache.device:
+    dev, d, nkv, c = _kv4_desc(cache, block_table)
+    if q.dim() != 3 or q.shape[0] != block_table.shape[0] or q.shape[2] != c:
         raise ValueError("q must be a bfloat16 [batch, nh, c] tensor on the cache's device")
-    nh = q.shape[1]
+    B, nh, _ = q.shape
+    qp = _dense(q, dev, torch.bfloat16, "q")
     if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
-        raise ValueError("out must be like q")
-    pp, _ = _kv4_pos(d, cache, pos, None)
-    sp = _dev_ptr(sink, q, torch.float32, "sink", nh)
-    with _On(cache):
-        if ws is None:
-            ws = torch.empty(max(csa_kv4_decode_workspace(nh, d.nkv, d.c), 16), dtype=torch.uint8,
-                             device=q.device)
-        _check(lib().csa_kv4_decode_attn(ctypes.byref(d), pp, _ptr(q), nh, int(window), int(first),
-                                         sp, float(scale), _ptr(out), _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream(q)))
+        out = torch.empty((B, nh, c), dtype=torch.bfloat16, device=q.device)
+    if ws is None:
+        if dev == torch._C._cuda_getDevice():
+            need = lib().csa_kv4_decode_workspace(nh, nkv, c)
+        else:
+            with torch.cuda.device(dev):
+                need = lib().csa_kv4_decode_workspace(nh, nkv, c)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a dense tensor on the cache's device")
+    _call(lib().csa_kv4_decode_attn, dev, ctypes.byref(d),
+          _dense(pos, dev, torch.int64, "pos", B), qp, nh, window, first,
+          _dense(sink, dev, torch.float32, "sink", nh), scale,
+          _dense(out, dev, torch.bfloat16, "out", B * nh * c), ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -654,34 +667,34 @@ def csa_blocks_copy(regions, src, dst, count: Optional[torch.Tensor] = None):
     copy of block src[i] (int32 lists on the device; ids outside the pool are
     skipped; count: int32, count[0] pairs).  No block may be a destination
     twice, nor both a source and a destination."""
-    regions = list(regions)
     if not regions:
         return
     if len(regions) > 16:
         raise ValueError("at most 16 regions")
-    nb, ref = regions[0].shape[0], regions[0]
+    dev, nb = _device(regions[0]), regions[0].shape[0]
     arr = (BlockRegion * len(regions))()
-    for i, r in enumerate(regions):
-        if r.shape[0] != nb or r.device != ref.device:
-            raise ValueError("regions must have the same blocks and device")
-        arr[i].base = _ptr(r)
-        arr[i].block_bytes = r.numel() // max(nb, 1) * r.element_size()
+    for a, r in zip(arr, regions):
+        if r.shape[0] != nb or r.get_device() != dev or not r.is_contiguous():
+            raise ValueError("regions must be dense and have the same blocks and device")
+        a.base, a.block_bytes = r.data_ptr(), r.nbytes // nb if nb else 0
     n = src.numel()
-    sp, dp = (_dev_ptr(x, ref, torch.int32, nm, n) for x, nm in ((src, "src"), (dst, "dst")))
-    cp = _dev_ptr(count, ref, torch.int32, "count")
-    with _On(ref):
-        _check(lib().csa_blocks_copy(arr, len(regions), nb, sp, dp, n, cp, _stream(ref)))
+    if count is not None and count.numel() < 1:
+        raise ValueError("count must have an element")
+    _call(lib().csa_blocks_copy, dev, arr, len(regions), nb,
+          _dense(src, dev, torch.int32, "src"), _dense(dst, dev, torch.int32, "dst", n), n,
+          _dense(count, dev, torch.int32, "count"))
 
 
 def _table(table: torch.Tensor, out: Optional[torch.Tensor]):
-    if table.dim() != 2 or table.dtype != torch.int32:
+    if table.dim() != 2:
         raise ValueError("table must be an int32 [rows, max_blocks] tensor")
+    dev = _device(table)
     if out is None:
-        out = torch.empty_like(table, memory_format=torch.contiguous_format)
+        out = torch.empty(table.shape, dtype=torch.int32, device=table.device)
     elif out.shape != table.shape:
         raise ValueError("table_out must be like table")
-    return _ptr(table), table.shape[0], table.shape[1], \
-        _dev_ptr(out, table, torch.int32, "table_out"), out
+    return dev, _dense(table, dev, torch.int32, "table"), *table.shape, \
+        _dense(out, dev, torch.int32, "table_out"), out
 
 
 def csa_blocks_fork(table, src, dst, tokens, fresh, block_tokens: int = 128,
@@ -690,16 +703,13 @@ def csa_blocks_fork(table, src, dst, tokens, fresh, block_tokens: int = 128,
     src[i]: whole blocks are shared, a partly filled last block becomes
     fresh[i].  Returns (table_out, copy_src, copy_dst); the copies (for
     csa_blocks_copy, once per cache) are -1 where there is nothing to copy."""
-    tp, rows, mb, op, out = _table(table, table_out)
+    dev, tp, rows, mb, op, out = _table(table, table_out)
     n = src.numel()
-    cs = torch.empty(n, dtype=torch.int32, device=table.device)
-    cd = torch.empty_like(cs)
-    ptrs = [_dev_ptr(x, table, dt, nm, n) for x, dt, nm in (
-        (src, torch.int32, "src"), (dst, torch.int32, "dst"), (tokens, torch.int64, "tokens"),
-        (fresh, torch.int32, "fresh"))]
-    with _On(table):
-        _check(lib().csa_blocks_fork(tp, rows, mb, *ptrs, n, int(block_tokens), op, _ptr(cs),
-                                     _ptr(cd), _stream(table)))
+    cs, cd = torch.empty((2, n), dtype=torch.int32, device=table.device)
+    i32 = torch.int32
+    _call(lib().csa_blocks_fork, dev, tp, rows, mb, _dense(src, dev, i32, "src"),
+          _dense(dst, dev, i32, "dst", n), _dense(tokens, dev, torch.int64, "tokens", n),
+          _dense(fresh, dev, i32, "fresh", n), n, block_tokens, op, cs.data_ptr(), cd.data_ptr())
     return out, cs, cd
 
 
@@ -707,13 +717,11 @@ def csa_blocks_free(table, seqs, num_blocks: int, table_out: Optional[torch.Tens
     """Rows ``seqs`` (int32) of the new table are -1.  Returns (table_out, freed,
     nfreed): the blocks no row names any more, ascending (int32 [num_blocks],
     -1 padded), and how many (int32 [1])."""
-    tp, rows, mb, op, out = _table(table, table_out)
+    dev, tp, rows, mb, op, out = _table(table, table_out)
     freed = torch.empty(num_blocks, dtype=torch.int32, device=table.device)
     n = torch.empty(1, dtype=torch.int32, device=table.device)
-    sp = _dev_ptr(seqs, table, torch.int32, "seqs")
-    with _On(table):
-        _check(lib().csa_blocks_free(tp, rows, mb, num_blocks, sp, seqs.numel(), op, _ptr(freed),
-                                     _ptr(n), _stream(table)))
+    _call(lib().csa_blocks_free, dev, tp, rows, mb, num_blocks,
+          _dense(seqs, dev, torch.int32, "seqs"), seqs.numel(), op, freed.data_ptr(), n.data_ptr())
     return out, freed, n
 
 
@@ -722,13 +730,11 @@ def csa_blocks_compact(table, num_blocks: int, table_out: Optional[torch.Tensor]
     copy_src, copy_dst, counts): the moves (int32 [num_blocks], -1 padded; for
     csa_blocks_copy with count=counts, once per cache) and counts = [moves,
     blocks in use]."""
-    tp, rows, mb, op, out = _table(table, table_out)
-    cs = torch.empty(num_blocks, dtype=torch.int32, device=table.device)
-    cd = torch.empty_like(cs)
+    dev, tp, rows, mb, op, out = _table(table, table_out)
+    cs, cd = torch.empty((2, num_blocks), dtype=torch.int32, device=table.device)
     counts = torch.empty(2, dtype=torch.int32, device=table.device)
-    with _On(table):
-        _check(lib().csa_blocks_compact(tp, rows, mb, num_blocks, op, _ptr(cs), _ptr(cd),
-                                        _ptr(counts), _stream(table)))
+    _call(lib().csa_blocks_compact, dev, tp, rows, mb, num_blocks, op, cs.data_ptr(),
+          cd.data_ptr(), counts.data_ptr())
     return out, cs, cd, counts
 
 

@@ -62,37 +62,60 @@ struct Quant8 {
   uint32_t E;
 };
 
-// Quantises 8 values of a row spread over `lanes` neighbouring lanes (8
-// values each, lane pairs (2 i, 2 i + 1) forming a group of 16).  Every lane
-// of the warp calls it.
-__device__ __forceinline__ Quant8 quantise8(const float v[8], int lanes) {
-  float a = 0.f;
-  bool bad = false;
+// Largest |x| of 8 values as bits (infinities and NaN order above all others).
+__device__ __forceinline__ uint32_t top_bits(const uint4& w) {  // bf16 pairs
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+  return max(a & 0xffff0000u, a << 16);
+}
+__device__ __forceinline__ uint32_t top_bits(const float v[8]) {
+  uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a = fmaxf(a, fabsf(v[i]));
-    bad |= !(fabsf(v[i]) <= 3.4028234664e38f);  // infinite or NaN
-  }
-  const float grp = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  float top = bad ? __int_as_float(0x7f800000) : grp;
-  for (int off = lanes >> 1; off > 0; off >>= 1)
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  const int ex = (int)(__float_as_uint(top) >> 23);
+  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+  return a;
+}
+
+// Quantises 8 values of a row spread over `lanes` neighbouring lanes (8
+// values each, lane pairs (2 i, 2 i + 1) forming a group of 16); a = their
+// top_bits.  Every lane of the warp calls it.
+//
+// The quotient x / (s r) without a division per value: x times the correctly
+// rounded reciprocal, corrected once by the exact remainder, is the correctly
+// rounded quotient, so a tie between two codes stays one, and adding 1.5 2^23
+// rounds it to nearest even.  A code can lie beyond 7 only for a subnormal s;
+// such groups, and rows near the ends of fp32's range, divide and clamp.
+__device__ __forceinline__ Quant8 quantise8(const float v[8], uint32_t a, int lanes) {
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  uint32_t top = a;
+  for (int off = lanes >> 1; off > 1; off >>= 1)
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const int ex = (int)(top >> 23);
   Quant8 q;
-  if (ex == 255) {
-    q.codes = 0x88888888u;
-    q.scale = 0;
-    q.E = 255;
-    return q;
-  }
+  q.codes = 0x88888888u;
+  q.scale = 0;
+  q.E = 255;
+  if (ex == 255) return q;
   q.E = (uint32_t)min(max(ex - 10, 1), 254);
   const float r = __uint_as_float(q.E << 23);
-  q.scale = e4m3_code(__fdiv_rn(grp, 7.f * r));
+  q.scale = e4m3_code(__fdiv_rn(__uint_as_float(a), 7.f * r));
   const float step = e4m3_value((uint8_t)q.scale) * r;
+  if (step == 0.f) return q;
+  if (q.scale >= 8 && q.E > 24 && q.E < 230) {
+    const float inv = __frcp_rn(step);
+    uint32_t acc = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const float t = v[i] * inv;
+      const float x = fmaf(fmaf(-t, step, v[i]), inv, t);
+      acc = acc * 16u + __float_as_uint(x + 12582920.f);  // 0x4b400000 + code + 8
+    }
+    q.codes = acc - 0x3f400000u;  // 0x4b400000 (1 + 16 + 16^2 + ...) mod 2^32
+    return q;
+  }
   q.codes = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = step > 0.f ? rintf(__fdiv_rn(v[i], step)) : 0.f;
+    const float x = rintf(__fdiv_rn(v[i], step));
     q.codes |= (uint32_t)((int)fminf(fmaxf(x, -7.f), 7.f) + 8) << (4 * i);
   }
   return q;

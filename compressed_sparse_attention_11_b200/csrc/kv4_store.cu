@@ -39,6 +39,39 @@ __device__ __forceinline__ uint8_t* image(const Kv4Rows& a, int64_t b, int h, in
                        (int64_t)kv4::tile_bytes(c);
 }
 
+// Eight consecutive values of a row as loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 w;
+  __device__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ uint32_t top() const { return kv4::top_bits(w); }
+  __device__ void unpack(float (&v)[8]) const {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(x[i] << 16);
+      v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  float w[8];
+  __device__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.f;
+  }
+  __device__ void load(const float* p) { load8(p, w); }
+  __device__ uint32_t top() const { return kv4::top_bits(w); }
+  __device__ void unpack(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
+  }
+};
+
 template <typename T, int C>
 __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const T* __restrict__ k,
                                                                 const T* __restrict__ v,
@@ -63,29 +96,38 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const T* __restr
   uint8_t* to = whole ? img[warp] : dst;
   const bool is_v = lane % (2 * L) >= L;
   const int sub = lane % L;
-  const T* src = is_v ? v : k;
+  const T* src = (is_v ? v : k) + h * C + sub * 8;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-#pragma unroll 4
-  for (int s = lo & ~(TS - 1); s < hi; s += TS) {
-    const int u = s + lane / (2 * L);
-    const bool on = u >= lo && u < hi;
-    float x[8];
+  const int64_t row0 = b * a.n + tile * 16 - p0;  // of the image's token 0
+  constexpr int U = sizeof(T) == 2 ? 8 : 4;       // rows in flight
+  for (int s0 = lo & ~(TS - 1); s0 < hi; s0 += TS * U) {
+    Raw<T> raw[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (on) load8(src + (b * a.n + tile * 16 + u - p0) * stride + h * C + sub * 8, x);
-    const kv4::Quant8 q = kv4::quantise8(x, L);
-    if (!on) continue;
-    const int slot = kv4::slot_of(u);
-    if (!is_v) {
-      *reinterpret_cast<uint32_t*>(to + slot * (C / 2) + sub * 4) = q.codes;
-      if ((sub & 1) == 0) to[kv4::off_ks(C) + slot * (C / 16) + sub / 2] = (uint8_t)q.scale;
-      if (sub == 0) to[kv4::off_exp(C) + 2 * slot] = (uint8_t)q.E;
-    } else {
-      uint8_t* vc = to + kv4::off_v(C);
-      *reinterpret_cast<uint16_t*>(vc + kv4::v_pair(C, u, sub * 8)) = (uint16_t)q.codes;
-      *reinterpret_cast<uint16_t*>(vc + kv4::v_pair(C, u, sub * 8 + 4)) = (uint16_t)(q.codes >> 16);
-      if ((sub & 1) == 0) to[kv4::off_vs(C) + (sub / 2) * 16 + u] = (uint8_t)q.scale;
-      if (sub == 0) to[kv4::off_exp(C) + 2 * slot + 1] = (uint8_t)q.E;
+    for (int i = 0; i < U; ++i) {
+      const int u = s0 + i * TS + lane / (2 * L);
+      raw[i].clear();
+      if (u >= lo && u < hi) raw[i].load(src + (row0 + u) * stride);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int s = s0 + i * TS, u = s + lane / (2 * L);
+      if (s >= hi) break;
+      float x[8];
+      raw[i].unpack(x);
+      const kv4::Quant8 q = kv4::quantise8(x, raw[i].top(), L);
+      if (u < lo || u >= hi) continue;
+      const int slot = kv4::slot_of(u);
+      if (!is_v) {
+        *reinterpret_cast<uint32_t*>(to + slot * (C / 2) + sub * 4) = q.codes;
+        if ((sub & 1) == 0) to[kv4::off_ks(C) + slot * (C / 16) + sub / 2] = (uint8_t)q.scale;
+        if (sub == 0) to[kv4::off_exp(C) + 2 * slot] = (uint8_t)q.E;
+      } else {
+        uint8_t* vc = to + kv4::off_v(C) + kv4::v_pair(C, u, sub * 8);
+        *reinterpret_cast<uint16_t*>(vc) = (uint16_t)q.codes;
+        *reinterpret_cast<uint16_t*>(vc + 4) = (uint16_t)(q.codes >> 16);
+        if ((sub & 1) == 0) to[kv4::off_vs(C) + (sub / 2) * 16 + u] = (uint8_t)q.scale;
+        if (sub == 0) to[kv4::off_exp(C) + 2 * slot + 1] = (uint8_t)q.E;
+      }
     }
   }
   if (whole) {

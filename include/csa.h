@@ -450,9 +450,10 @@ csa_status csa_paged_decode_step(const csa_cache_desc* desc, const csa_paging* p
  *       its input with the same stride (in place), and must not overlap
  *       another tensor of the call otherwise
  *   nh = 0 or nkv = 0 leaves that tensor out (its pointers are ignored).
- * Needs c <= 512 (above 256: c % 16 == 0); the halves form rope_dims % 16 == 0
- * (% 32 above c = 256), else CSA_ERR_UNSUPPORTED.  Strides: whole 16-byte
- * units.  Norm, angle (double) and rotation in fp32, one rounding to `dt`.
+ * Needs c <= 512 (above 256: c % 16 == 0, and rope_dims % 16 == 0 in the
+ * halves form), else CSA_ERR_UNSUPPORTED.
+ * Strides: whole 16-byte units.  Norm, angle (double) and rotation in fp32,
+ * one rounding to `dt`.
  * ------------------------------------------------------------------------ */
 typedef struct {
   const float* q_gamma; /* [c], or [nh][c] with per_head; NULL: no norm of q   */

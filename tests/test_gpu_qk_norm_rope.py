@@ -56,6 +56,11 @@ def run(T, nh, nkv, c, R, halves, sections, dt, per_head, gamma, far, packed, in
     (21, 7, 3, 72, 72, False, (9, 9, 9, 9), torch.bfloat16, False, True, False),
     (4, 2, 2, 8, 8, False, (4,), torch.bfloat16, False, False, False),
     (33, 2, 2, 272, 32, True, (16,), torch.bfloat16, False, False, False),
+    (33, 2, 2, 64, 24, True, (5, 7), torch.bfloat16, True, False, True),
+    (3, 9, 3, 400, 80, True, (40,), torch.float32, False, False, False),
+    (7, 3, 2, 80, 40, False, (11, 9), torch.bfloat16, True, False, False),
+    (3, 9, 3, 400, 40, False, (20,), torch.bfloat16, False, True, False),
+    (2500, 40, 3, 128, 128, True, (64,), torch.bfloat16, True, False, False),
 ])
 def test_matches_definition(T, nh, nkv, c, R, halves, sections, dt, per_head, packed, inplace):
     run(T, nh, nkv, c, R, halves, sections, dt, per_head, True, 50, packed, inplace)

@@ -63,7 +63,7 @@ def rope(**kw):
     (dict(pos=ODD), BAD, "pos is misaligned"),
     (dict(c=520, qs=8320, qos=8320, ks=1040, kos=1040), UNSUP, "c <= 512"),
     (dict(c=264, qs=2112, qos=2112, ks=528, kos=528), UNSUP, "multiple of 16"),
-    (dict(R=24, halves=1, sec=(12, 0, 0, 0)), UNSUP, "halves"),
+    (dict(c=272, R=24, halves=1, sec=(12, 0, 0, 0), qs=2176, qos=2176, ks=544, kos=544), UNSUP, "rope_dims as well"),
     (dict(nh=70000, qs=70000 * 128, qos=70000 * 128), UNSUP, "65536"),
 ])
 def test_qk_norm_rope_refuses(kw, status, reason):
