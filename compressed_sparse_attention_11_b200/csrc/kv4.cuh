@@ -6,13 +6,13 @@
 //   each 16 values: s = E4M3(max|x| / (7 r)), code = rint(x / (s r)) in -7 .. 7
 //       (0 when s = 0), stored as the nibble code + 8;
 //   value = r s code.
-// s has 4 significant bits and a code 3, so s * code is exact in bf16: the
-// operands of the attention's matrix instructions are exact, and r, a power
-// of two per row, goes onto the logit (K) or the softmax weight (V).  With
-// bf16 x no rounding decision can fall differently in fp32 than in exact
-// arithmetic: a quotient of x by the <= 7-bit product 7 r t or t s r is a tie
-// only when it is one exactly, and is at least 2^-9 away (relative)
-// otherwise.
+// s has 4 significant bits and a code 3, so s * code is exact in 16-bit
+// floats: the operands of the attention's matrix instructions are exact, and
+// r, a power of two per row, goes onto the logit (K) or the softmax weight
+// (V).  A row with E = 255 has all codes 0 and s = 0.  With bf16 x no rounding
+// decision can fall differently in fp32 than in exact arithmetic: a quotient
+// of x by the <= 7-bit product 7 r t or t s r is a tie only when it is one
+// exactly, and is at least 2^-9 away (relative) otherwise.
 //
 // 16 consecutive tokens of one head are one tile image (tile_bytes):
 //   K codes  [slot][c / 2]              slot(u) = 8 h + 2 t + b of token u = 4 t + 2 h + b

@@ -6,26 +6,37 @@
 //
 // HBM-bound up to g = 16 (146 bytes a token and head at c = 128 against 8 g c
 // flops); what it takes is turning 4-bit codes into matrix operands as fast
-// as they arrive.  Both products run on mma.sync.m16n8k16 with the cache on
-// the M side and the heads on the N side (8 heads a tile), so no row of the
-// instruction is padding at g = 8:
-//   S^T[key, head] = K Q^T,   O^T[dim, head] += V^T P^T,
-// and a code pair becomes an operand register in three instructions: shift,
-// (x & mask) | 1.0 (the nibble n lands in the upper mantissa bits of a bf16:
-// 1 + n / 16), and one bf16x2 fma with (16 s, -24 s), which gives s (n - 8)
-// exactly.  The format stores rows in the fragments' order, so V needs no
-// transposition, and the row exponents go onto the logit and the weight.
+// as they arrive.  Both products run on mma.sync.m16n8k16 (f16 in, fp32 out)
+// with the cache on the M side and the heads on the N side (8 heads a tile),
+// so no row of the instruction is padding at g = 8:
+//   S^T[key, head] = K Q^T,   O^T[dim, head] += V^T P^T.
+// The format stores rows in the fragments' order, so V needs no transposition,
+// and a nibble becomes an operand where it stands: in a 16-bit word of four,
+// (x & 0x00f0) | 0x5400 is the f16 64 + n and one fma with (s, -72 s) gives
+// s (n - 8) exactly; (x & 0x000f) | 0x6400 is 1024 + n and takes a subtraction
+// and a product; the upper two follow after one shift.  Logic and shifts run
+// at half the rate of the fmas here, and were the bound with bf16 operands,
+// whose seven mantissa bits want a shift per nibble.
+// f16's range: a query head is scaled to largest element 1 .. 2 (elements below
+// 2^-14 of it keep an absolute 2^-25), and the second product's weight is
+// w_u = 2^(l_u + E_u - M'), E_u the value row's exponent and M' a running
+// maximum of its own, so that the rows that make up the output have weights
+// near 1 whatever their magnitude.
 // tcgen05 would need the widened rows in shared memory first (16-bit operands
 // of both products through it: four times the cache's bytes), which is more
 // than an SM's share of HBM time allows; mma.sync takes them from registers.
 //
 // Work: units of 8 images (128 tokens) of one (sequence, head tile), in one
-// flat list that is cut evenly over the CTAs whatever the lengths; a producer
-// warp streams units through a ring of bulk copies, warp w of 8 takes image w
-// of each unit with its own running maximum, sum and output, and the eight
+// flat list that is cut evenly over the CTAs whatever the lengths.  Warp w of
+// 8 takes image w of each unit, brought in by bulk copies through a ring of
+// its own, so no warp waits for another (with one ring for the CTA the warps
+// moved in step: 302 us where this takes XX, 32 sequences of 16-32 K tokens,
+// 64 / 8 heads x 128), with its own running maxima, sum and output; the eight
 // are merged where a sequence ends or the CTA's share does.  What a CTA covers
 // whole is written out; other pieces go to the workspace (two slots a CTA) and
 // a second kernel merges them.
+#include <limits.h>
+
 #include "api_check.h"
 #include "common.cuh"
 #include "kv4.cuh"
@@ -38,11 +49,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kConsWarps = 8;
-constexpr int kConsThreads = kConsWarps * 32;
-constexpr int kThreads = kConsThreads + 32;
-constexpr int kUnitTiles = kConsWarps;  // images per unit
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnitTiles = kWarps;  // images per unit
 constexpr float kRescaleLog2 = 8.f;
+constexpr float kNone = -3e38f;  // running maximum of a head that has seen nothing
 
 struct DecArgs {
   const uint8_t* cache;
@@ -53,33 +64,32 @@ struct DecArgs {
   __nv_bfloat16* out;
   float* ws;
   unsigned int* err;
-  int64_t max_blocks, num_blocks, capacity;  // capacity: tokens a row of the table can name
-  int64_t window, first;
+  int64_t max_blocks, num_blocks;
+  int capacity;  // tokens a row of the table can name
+  int window, first;
   int batch, nkv, nh, group, head_tiles, tiles_per_block;
   float qscale;  // scale * log2(e)
 };
 
-// What sequence b sees, in images: virtual image i is image i below `head`,
-// else image tail + i - head.
+// Positions are below 2^31 - 1 (a sequence holds at most 2^31 tokens).
+__device__ __forceinline__ int clip_pos(int64_t p) {
+  return (int)max((int64_t)-1, min(p, (int64_t)INT_MAX - 1));
+}
+// What the query at position p sees, in images: virtual image i is image i
+// below `head`, else image tail + i - head.
 struct Seen {
-  int64_t n, lo;  // visible: u < n and (u >= lo or u < first)
+  int n, lo;  // visible: u < n and (u >= lo or u < first)
   int head, tail, images;
 };
-__device__ __forceinline__ Seen seen_of(const DecArgs& a, int64_t p) {
+__device__ __forceinline__ Seen seen_of(const DecArgs& a, int p) {
   Seen s;
-  s.n = min(p + 1, a.capacity);
-  s.lo = 0;
-  s.head = s.tail = s.images = 0;
-  if (p < 0) {
-    s.n = 0;
-    return s;
-  }
-  if (a.window > 0 && p + 1 > a.window) s.lo = p + 1 - a.window;
-  const int64_t end = (s.n + 15) / 16;
-  const int64_t t = min(s.lo / 16, end), h = (min(a.first, s.lo) + 15) / 16;
-  s.tail = (int)t;
-  s.head = (int)min(h, t);
-  s.images = s.head + (int)(end - t);
+  s.n = min(p + 1, a.capacity);  // 0 for p = -1
+  s.lo = a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
+  const int end = s.n / 16 + (s.n % 16 != 0);
+  const int h = min(a.first, s.lo);
+  s.tail = min(s.lo / 16, end);
+  s.head = min(h / 16 + (h % 16 != 0), s.tail);
+  s.images = s.head + (end - s.tail);
   return s;
 }
 __device__ __forceinline__ int units_of(const Seen& s) {
@@ -96,7 +106,7 @@ __device__ __forceinline__ int cta_of(int64_t U, int G, int64_t u) {
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -106,49 +116,79 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 
-// Scale bytes picked into the two halves -> (16 s, -24 s).  An E4M3 byte
-// shifted into a bf16's exponent and mantissa reads as s 2^-120.
-struct ScalePair {
-  uint32_t s16, n24;
+// f16 pairs kept in registers (a logic instruction takes one immediate, the
+// mask; the others would be fetched anew at each use).
+struct Bases {
+  uint32_t k1024, k64, m1032, m72;
 };
-__device__ __forceinline__ ScalePair scale_pair(uint32_t bytes, uint32_t sel) {
+__device__ __forceinline__ Bases bases() {
+  Bases k{0x64006400u, 0x54005400u, 0xe408e408u, 0xd480d480u};
+  asm volatile("" : "+r"(k.k1024), "+r"(k.k64), "+r"(k.m1032), "+r"(k.m72));
+  return k;
+}
+// Scale bytes picked into the two halves -> (s, -72 s) 2^-8: an E4M3 byte
+// shifted into an f16's exponent and mantissa reads as s 2^-8.
+struct ScalePair {
+  uint32_t s, n72;
+};
+__device__ __forceinline__ ScalePair scale_pair(uint32_t bytes, uint32_t sel, const Bases& k) {
   ScalePair p;
-  p.s16 = mul_bf16x2(__byte_perm(bytes, 0, sel) << 4, 0x7d807d80u);  // 2^124
-  p.n24 = mul_bf16x2(p.s16, 0xbfc0bfc0u);                            // -1.5
+  p.s = __byte_perm(bytes, 0, sel) << 7;
+  p.n72 = mul_f16x2(p.s, k.m72);
   return p;
 }
-// Nibbles j and j + 4 of w -> (s (n - 8)) in the two halves.
-template <int J>
-__device__ __forceinline__ uint32_t widen(uint32_t w, const ScalePair& s) {
-  const uint32_t y = J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3);
-  return fma_bf16x2((y & 0x00780078u) | 0x3f803f80u, s.s16, s.n24);
+// Nibbles j and j + 4 of w, j = 0 .. 3 -> s (n - 8) 2^-8 in the two halves.
+__device__ __forceinline__ void widen4(uint32_t w, const ScalePair& s, const Bases& k,
+                                       uint32_t (&v)[4]) {
+  const uint32_t y = w >> 8;
+  v[0] = mul_f16x2(add_f16x2((w & 0x000f000fu) | k.k1024, k.m1032), s.s);
+  v[1] = fma_f16x2((w & 0x00f000f0u) | k.k64, s.s, s.n72);
+  v[2] = mul_f16x2(add_f16x2((y & 0x000f000fu) | k.k1024, k.m1032), s.s);
+  v[3] = fma_f16x2((y & 0x00f000f0u) | k.k64, s.s, s.n72);
+}
+
+// A piece's state per head: running maximum M of the logits (log2 units), sum
+// L of 2^(l - M), and the reference MV of the output's weights.
+__device__ __forceinline__ float out_factor(float M, float L, float MV, const float* sink, int head) {
+  if (M == kNone) return L == 0.f ? 0.f : L;  // nothing seen: zeros (a NaN sum stays one)
+  const float den = L + (sink != nullptr ? ex2(sink[head] * kLog2e - M) : 0.f);
+  return ex2(MV - M - (127.f - 8.f)) / den;  // E's bias, and the scales' 2^-8
 }
 
 template <int C, int NT>
 struct Cfg {
   static constexpr int kTB = kv4::tile_bytes(C);
-  static constexpr int kStageBytes = kUnitTiles * kTB;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = 4;  // images in a warp's ring
   static constexpr int kHeads = 8 * NT;
   static constexpr int kLd = C + 4;  // padded row of the merge buffer (floats)
-  static constexpr int kSlot = kHeads * C + 2 * kHeads;  // floats of a workspace slot
-  static constexpr int off_merge() { return kStages * kStageBytes; }
-  static constexpr int off_ml() { return off_merge() + kConsWarps * kHeads * kLd * 4; }
-  static constexpr int off_meta() { return off_ml() + kConsWarps * kHeads * 8; }
-  static constexpr int off_bar() { return off_meta() + kStages * kUnitTiles * 8; }
-  static constexpr int off_list() { return off_bar() + 2 * kStages * 8 + 16 + 64; }
-  static size_t smem(int batch) { return off_list() + (size_t)(batch + 1) * 4; }
+  static constexpr int kSlot = kHeads * C + 4 * kHeads;  // floats of a workspace slot
+  static constexpr int off_merge() { return kWarps * kStages * kTB; }
+  static constexpr int off_ml() { return off_merge() + kWarps * kHeads * kLd * 4; }
+  static constexpr int off_meta() { return off_ml() + kWarps * kHeads * 16; }
+  static constexpr int off_bar() { return off_meta() + kWarps * kStages * 4; }
+  static constexpr int off_list() { return off_bar() + kWarps * kStages * 8 + 64; }
+  static size_t smem(int batch) { return off_list() + (size_t)(2 * batch + 1) * 4; }
 };
 
 template <int C, int NT>
@@ -159,21 +199,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
   constexpr int MT = D / 2;   // m-tiles of P.V
   extern __shared__ __align__(128) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + F::off_merge());
-  float2* ml = reinterpret_cast<float2*>(smem + F::off_ml());
-  int64_t* meta = reinterpret_cast<int64_t*>(smem + F::off_meta());  // first token, or -1
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::off_bar());
-  uint64_t* empty = full + F::kStages;
-  int* scan = reinterpret_cast<int*>(empty + F::kStages);
-  int* first_unit = reinterpret_cast<int*>(smem + F::off_list());  // [batch + 1]
+  float4* ml = reinterpret_cast<float4*>(smem + F::off_ml());  // (M, L, MV, -)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * F::kStages * F::kTB;
+  int* meta = reinterpret_cast<int*>(smem + F::off_meta()) + warp * F::kStages;  // first token, or -1
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::off_bar()) + warp * F::kStages;
+  int* scan = reinterpret_cast<int*>(smem + F::off_bar() + kWarps * F::kStages * 8);
+  int* first_unit = reinterpret_cast<int*>(smem + F::off_list());  // [batch + 1]
+  int* position = first_unit + a.batch + 1;                         // [batch]
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < F::kStages; ++i) {
-      mbar_init(&full[i], kUnitTiles);
-      mbar_init(&empty[i], kConsWarps);
-    }
+  if (lane == 0) {
+    for (int i = 0; i < F::kStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
 
@@ -182,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
     int base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      const int u = b < a.batch ? units_of(seen_of(a, a.pos[b])) : 0;
+      const int p = b < a.batch ? clip_pos(a.pos[b]) : -1;
+      const int u = units_of(seen_of(a, p));
       int inc = u;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -196,7 +236,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
         if (w < warp) before += scan[w];
         all += scan[w];
       }
-      if (b < a.batch) first_unit[b] = before + inc - u;
+      if (b < a.batch) {
+        first_unit[b] = before + inc - u;
+        position[b] = p;
+      }
       base += all;
       __syncthreads();
     }
@@ -212,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
   const int64_t u_lo = cta_first(U, G, blockIdx.x), u_hi = cta_first(U, G, blockIdx.x + 1);
 
   // the sequence of the first unit: the last b with HV * first_unit[b] <= u_lo
-  int b = 0;
+  int b;
   {
     int lo = 0, hi = a.batch;  // first_unit[lo] * HV <= u_lo < first_unit[hi] * HV
     while (hi - lo > 1) {
@@ -222,222 +265,298 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
     }
     b = lo;
   }
-  int nu = first_unit[b + 1] - first_unit[b];
-  int64_t off = u_lo - (int64_t)first_unit[b] * HV;
-  int hv = (int)(off / nu), s = (int)(off - (int64_t)hv * nu);
-  auto next_segment = [&]() {  // the unit list's next (sequence, head tile)
-    s = 0;
-    if (++hv == HV) {
-      hv = 0;
-      do { ++b; } while (b < a.batch && first_unit[b + 1] == first_unit[b]);
-      nu = b < a.batch ? first_unit[b + 1] - first_unit[b] : 0;
+  // a place in the unit list: unit s of the nu units of (sequence b, head tile hv)
+  struct Place {
+    int b, hv, s, nu;
+  };
+  auto next_segment = [&](Place& p) {
+    p.s = 0;
+    if (++p.hv == HV) {
+      p.hv = 0;
+      do { ++p.b; } while (p.b < a.batch && first_unit[p.b + 1] == first_unit[p.b]);
+      p.nu = p.b < a.batch ? first_unit[p.b + 1] - first_unit[p.b] : 0;
     }
   };
-
-  if (warp == kConsWarps) {
-    // ============================ producer: lanes 0-7, one image each ==========
-    int it = 0;
-    for (int64_t u = u_lo; u < u_hi;) {
-      const Seen v = seen_of(a, a.pos[b]);
-      const int h = hv / a.head_tiles;
-      for (; s < nu && u < u_hi; ++s, ++u, ++it) {
-        const int st = it % F::kStages;
-        const int i = s * kUnitTiles + lane;
-        int64_t tile = -1, blk = -1;
-        if (lane < kUnitTiles && i < v.images) {
-          tile = i < v.head ? i : v.tail + (i - v.head);
-          blk = a.table[b * a.max_blocks + tile / a.tiles_per_block];
-          if (blk < 0 || blk >= a.num_blocks) tile = -1;
-        }
-        if (it >= F::kStages) mbar_wait(&empty[st], ((it / F::kStages) - 1) & 1, a.err);
-        if (lane < kUnitTiles) {
-          meta[st * kUnitTiles + lane] = tile < 0 ? -1 : tile * 16;
-          if (tile >= 0) {
-            mbar_arrive_expect_tx(&full[st], F::kTB);
-            bulk_load(smem + st * F::kStageBytes + lane * F::kTB,
-                      a.cache + ((blk * a.nkv + h) * a.tiles_per_block +
-                                 tile % a.tiles_per_block) * (int64_t)F::kTB,
-                      F::kTB, &full[st]);
-          } else {
-            mbar_arrive(&full[st]);
-          }
-        }
-        __syncwarp();
-      }
-      if (s == nu) next_segment();
-    }
-    // after a wait that gave up, copies may still be on their way in
-    const int last = it < F::kStages ? it : F::kStages;
-    for (int k = it - last; k < it; ++k)
-      mbar_wait(&full[k % F::kStages], (k / F::kStages) & 1, a.err, false);
-    return;
+  Place at;
+  at.b = b;
+  at.nu = first_unit[b + 1] - first_unit[b];
+  {
+    const int64_t off = u_lo - (int64_t)first_unit[b] * HV;
+    at.hv = (int)(off / at.nu);
+    at.s = (int)(off - (int64_t)at.hv * at.nu);
   }
+  const int units = (int)min(u_hi - u_lo, (int64_t)INT_MAX);
+
+  // ---- this warp's images, looked up 32 units at a time: lane i those of
+  // unit base + i (the block numbers are on their way until they are used) ----
+  Place look = at;  // the first unit of the batch to come
+  int look_unit = 0;
+  int t0_c = -1, img_c = 0;                  // this batch: first token (-1: none), image number
+  int tile_n = -1, blk_n = -1, row_n = 0;     // the next
+  auto look_up = [&]() {
+    t0_c = tile_n >= 0 && blk_n >= 0 && blk_n < a.num_blocks ? tile_n * 16 : -1;
+    img_c = blk_n * a.nkv * a.tiles_per_block + row_n;
+    tile_n = -1;
+    if (look_unit >= units) return;
+    Place p = look;
+    if (look_unit + lane < units) {
+      p.s += lane;
+      while (p.s >= p.nu) {
+        const int rest = p.s - p.nu;
+        next_segment(p);
+        p.s = rest;
+      }
+      const Seen v = seen_of(a, position[p.b]);
+      const int i = p.s * kUnitTiles + warp;
+      if (i < v.images) {
+        tile_n = i < v.head ? i : v.tail + (i - v.head);
+        const int j = tile_n / a.tiles_per_block;
+        row_n = (p.hv / a.head_tiles) * a.tiles_per_block + tile_n - j * a.tiles_per_block;
+        blk_n = __ldg(a.table + p.b * a.max_blocks + j);
+      }
+    }
+    look_unit += 32;
+    if (look_unit < units) {
+      look.s += 32;
+      while (look.s >= look.nu) {
+        const int rest = look.s - look.nu;
+        next_segment(look);
+        look.s = rest;
+      }
+    }
+  };
+  auto issue = [&](int u, int st) {  // the image of unit u into its stage, which is free
+    if (u >= units) return;
+    if ((u & 31) == 0 && u > 0) look_up();
+    const int t0 = __shfl_sync(0xffffffffu, t0_c, u & 31);
+    const int img = __shfl_sync(0xffffffffu, img_c, u & 31);
+    if (lane == 0) {
+      meta[st] = t0;
+      if (t0 >= 0) {
+        mbar_arrive_expect_tx(&full[st], F::kTB);
+        bulk_load(ring + st * F::kTB, a.cache + (int64_t)img * F::kTB, F::kTB, &full[st]);
+      } else {
+        mbar_arrive(&full[st]);
+      }
+    }
+  };
+  look_up();
+  look_up();
+  for (int u = 0; u < F::kStages; ++u) issue(u, u);
 
   // ============================== consumers ====================================
   const int gid = lane >> 2, tig = lane & 3;
   const int tok_a = 4 * (gid >> 1) + (gid & 1);  // token of slot gid; slot gid + 8: + 2
-  int it = 0;
-  for (int64_t u = u_lo; u < u_hi;) {
-    const Seen v = seen_of(a, a.pos[b]);
-    const int kvh = hv / a.head_tiles, h0 = (hv % a.head_tiles) * F::kHeads;
-    const int cur_b = b, cur_hv = hv;
-    const bool starts = s == 0, at_first = u == u_lo;
-    // queries as B fragments: head gid (+ 8 per n-tile), dims C / 4 tig ..
+  for (int u = 0; u < units;) {
+    const Seen v = seen_of(a, position[at.b]);
+    const int seen_n = v.n, seen_lo = v.lo, seen_first = a.first;
+    const int kvh = at.hv / a.head_tiles, h0 = (at.hv % a.head_tiles) * F::kHeads;
+    const int cur_b = at.b;
+    const bool starts = at.s == 0, at_first = u == 0;
+    // queries as B fragments: head gid (+ 8 per n-tile), dims C / 4 tig ..,
+    // scaled by a power of two per head
     uint32_t qf[NT][KS][2];
+    float qfac[NT][2];  // of heads 2 tig, 2 tig + 1: scale * log2(e) * 2^8 over that power
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int hl = h0 + 8 * t + gid;
       const __nv_bfloat16* qp =
           a.q + ((int64_t)cur_b * a.nh + (int64_t)kvh * a.group + hl) * C + tig * (C / 4);
+      uint4 raw[C / 32];
+      uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < C / 32; ++w) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (hl < a.group) r = __ldg(reinterpret_cast<const uint4*>(qp) + w);
-        qf[t][2 * w][0] = __byte_perm(r.x, r.z, 0x5410);
-        qf[t][2 * w][1] = __byte_perm(r.x, r.z, 0x7632);
-        qf[t][2 * w + 1][0] = __byte_perm(r.y, r.w, 0x5410);
-        qf[t][2 * w + 1][1] = __byte_perm(r.y, r.w, 0x7632);
+        raw[w] = make_uint4(0, 0, 0, 0);
+        if (hl < a.group) raw[w] = __ldg(reinterpret_cast<const uint4*>(qp) + w);
+        top = max(top, kv4::top_bits(raw[w]));
       }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(127 - exponent): the largest element becomes 1 .. 2 (a head of zeros
+      // or with an element that is not finite stays as it is)
+      const uint32_t e = top >> 23;
+      const bool plain = e == 0 || e == 255;
+      const float up = plain ? 1.f : __uint_as_float(e == 254 ? 1u << 22 : (254u - e) << 23);
+      const float back = (plain ? 1.f : __uint_as_float(e << 23)) * (a.qscale * 256.f);
+#pragma unroll
+      for (int w = 0; w < C / 32; ++w) {
+        const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __uint_as_float(r[i] << 16) * up;
+          x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u) * up;
+        }
+        qf[t][2 * w][0] = pack_f16x2(x[0], x[4]);
+        qf[t][2 * w][1] = pack_f16x2(x[1], x[5]);
+        qf[t][2 * w + 1][0] = pack_f16x2(x[2], x[6]);
+        qf[t][2 * w + 1][1] = pack_f16x2(x[3], x[7]);
+      }
+      qfac[t][0] = __shfl_sync(0xffffffffu, back, 8 * tig);
+      qfac[t][1] = __shfl_sync(0xffffffffu, back, 8 * tig + 4);
     }
     float o[NT][MT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], mv[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = kNegInf;
+      m[t][0] = m[t][1] = mv[t][0] = mv[t][1] = kNone;
       l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int k = 0; k < MT; ++k) o[t][k][0] = o[t][k][1] = o[t][k][2] = o[t][k][3] = 0.f;
     }
 
-    for (; s < nu && u < u_hi; ++s, ++u, ++it) {
-      const int st = it % F::kStages;
-      mbar_wait(&full[st], (it / F::kStages) & 1, a.err);
-      const int64_t t0 = meta[st * kUnitTiles + warp];
-      if (t0 >= 0) {
-        const uint8_t* im = smem + st * F::kStageBytes + warp * F::kTB;
-        // ---- S^T = K Q^T ----------------------------------------------------
-        float sc[NT][4];
+    const Bases k16 = bases();
+    auto image = [&](const uint8_t* im, int t0) {
+      // ---- S^T = K Q^T ----------------------------------------------------
+      float sc[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
-        uint32_t ka[C / 32], kb[C / 32];
-        ScalePair sa[C / 64], sb[C / 64];
-        if constexpr (C == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(im + gid * 64 + tig * 16);
-          const uint4 y = *reinterpret_cast<const uint4*>(im + (gid + 8) * 64 + tig * 16);
-          ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
-          kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
-          const uint32_t p = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + gid * 8 + 2 * tig);
-          const uint32_t r = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + (gid + 8) * 8 + 2 * tig);
-          sa[0] = scale_pair(p, 0x4040); sa[1] = scale_pair(p, 0x4141);
-          sb[0] = scale_pair(r, 0x4040); sb[1] = scale_pair(r, 0x4141);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(im + gid * 32 + tig * 8);
-          const uint2 y = *reinterpret_cast<const uint2*>(im + (gid + 8) * 32 + tig * 8);
-          ka[0] = x.x; ka[1] = x.y;
-          kb[0] = y.x; kb[1] = y.y;
-          sa[0] = scale_pair(im[kv4::off_ks(C) + gid * 4 + tig], 0x4040);
-          sb[0] = scale_pair(im[kv4::off_ks(C) + (gid + 8) * 4 + tig], 0x4040);
+      for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+      uint32_t ka[C / 32], kb[C / 32];
+      ScalePair sa[C / 64], sb[C / 64];
+      if constexpr (C == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(im + gid * 64 + tig * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(im + (gid + 8) * 64 + tig * 16);
+        ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
+        kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
+        const uint32_t p = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + gid * 8 + 2 * tig);
+        const uint32_t r = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + (gid + 8) * 8 + 2 * tig);
+        sa[0] = scale_pair(p, 0x4040, k16); sa[1] = scale_pair(p, 0x4141, k16);
+        sb[0] = scale_pair(r, 0x4040, k16); sb[1] = scale_pair(r, 0x4141, k16);
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(im + gid * 32 + tig * 8);
+        const uint2 y = *reinterpret_cast<const uint2*>(im + (gid + 8) * 32 + tig * 8);
+        ka[0] = x.x; ka[1] = x.y;
+        kb[0] = y.x; kb[1] = y.y;
+        sa[0] = scale_pair(im[kv4::off_ks(C) + gid * 4 + tig], 0x4040, k16);
+        sb[0] = scale_pair(im[kv4::off_ks(C) + (gid + 8) * 4 + tig], 0x4040, k16);
+      }
+      const uint32_t ea = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid);
+      const uint32_t eb = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid + 16);
+#pragma unroll
+      for (int w = 0; w < C / 32; ++w) {
+        uint32_t ra[4], rb[4];
+        widen4(ka[w], sa[w / 2], k16, ra);
+        widen4(kb[w], sb[w / 2], k16, rb);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mma_16816(sc[t], ra[0], rb[0], ra[1], rb[1], qf[t][2 * w][0], qf[t][2 * w][1]);
+          mma_16816(sc[t], ra[2], rb[2], ra[3], rb[3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
         }
+      }
+      // ---- online softmax: l, and l + E of the value row ----------------------
+      const float ka_r = __uint_as_float((ea & 255u) << 23), kb_r = __uint_as_float((eb & 255u) << 23);
+      // E as a float; infinite for a row that is not finite (0 w then makes NaN)
+      const float va_e = ea >= 0xff00u ? __int_as_float(0x7f800000) : (float)(ea >> 8);
+      const float vb_e = eb >= 0xff00u ? __int_as_float(0x7f800000) : (float)(eb >> 8);
+      float lv[NT][4];
+      bool grow = false;
 #pragma unroll
-        for (int w = 0; w < C / 32; ++w) {
-          const uint32_t a0 = widen<0>(ka[w], sa[w / 2]), a1 = widen<0>(kb[w], sb[w / 2]);
-          const uint32_t a2 = widen<1>(ka[w], sa[w / 2]), a3 = widen<1>(kb[w], sb[w / 2]);
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma_16816(sc[t], a0, a1, a2, a3, qf[t][2 * w][0], qf[t][2 * w][1]);
-          const uint32_t c0 = widen<2>(ka[w], sa[w / 2]), c1 = widen<2>(kb[w], sb[w / 2]);
-          const uint32_t c2 = widen<3>(ka[w], sa[w / 2]), c3 = widen<3>(kb[w], sb[w / 2]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma_16816(sc[t], c0, c1, c2, c3, qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+        for (int e = 0; e < 2; ++e) {
+          sc[t][e] = sc[t][e] * ka_r * qfac[t][e];
+          sc[t][2 + e] = sc[t][2 + e] * kb_r * qfac[t][e];
+          lv[t][e] = sc[t][e] + va_e;
+          lv[t][2 + e] = sc[t][2 + e] + vb_e;
         }
-        // ---- online softmax ---------------------------------------------------
-        const uint32_t ea = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid);
-        const uint32_t eb = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid + 16);
-        const int64_t ua = t0 + tok_a, ub = ua + 2;
-        const bool va = ua < v.n && (ua >= v.lo || ua < a.first);
-        const bool vb = ub < v.n && (ub >= v.lo || ub < a.first);
-        const float ra = kv4::row_scale(ea & 255u) * a.qscale, rb = kv4::row_scale(eb & 255u) * a.qscale;
-        const float wa = va ? kv4::row_scale(ea >> 8) : 0.f, wb = vb ? kv4::row_scale(eb >> 8) : 0.f;
-        bool grow = false;
+      if (t0 + 15 >= seen_n || (t0 < seen_lo && t0 + 15 >= seen_first)) {  // some row is hidden
+        const int ua = t0 + tok_a, ub = ua + 2;
+        const bool sa_ = ua < seen_n && (ua >= seen_lo || ua < seen_first);
+        const bool sb_ = ub < seen_n && (ub >= seen_lo || ub < seen_first);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            sc[t][e] = va ? sc[t][e] * ra : kNegInf;
-            sc[t][2 + e] = vb ? sc[t][2 + e] * rb : kNegInf;
-            grow |= fmaxf(sc[t][e], sc[t][2 + e]) > m[t][e] + kRescaleLog2;
+            if (!sa_) sc[t][e] = lv[t][e] = kNegInf;
+            if (!sb_) sc[t][2 + e] = lv[t][2 + e] = kNegInf;
           }
-        if (__any_sync(0xffffffffu, grow)) {
+      }
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(sc[t][e], sc[t][2 + e]);
+        for (int e = 0; e < 2; ++e)
+          grow |= fmaxf(sc[t][e], sc[t][2 + e]) > m[t][e] + kRescaleLog2 ||
+                  fmaxf(lv[t][e], lv[t][2 + e]) > mv[t][e] + kRescaleLog2;
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-              for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-              x = fmaxf(x, m[t][e]);
-              const float f = m[t][e] == kNegInf ? 0.f : ex2(m[t][e] - x);
-              m[t][e] = x;
-              l[t][e] *= f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(sc[t][e], sc[t][2 + e]), y = fmaxf(lv[t][e], lv[t][2 + e]);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+            }
+            x = fmaxf(x, m[t][e]);
+            y = fmaxf(y, mv[t][e]);
+            if (x > m[t][e]) l[t][e] *= ex2(m[t][e] - x);
+            m[t][e] = x;
+            if (y > mv[t][e]) {
+              const float f = ex2(mv[t][e] - y);
+              mv[t][e] = y;
 #pragma unroll
               for (int k = 0; k < MT; ++k) {
                 o[t][k][e] *= f;
                 o[t][k][2 + e] *= f;
               }
             }
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[t][e] += ex2(sc[t][e] - m[t][e]) + ex2(sc[t][2 + e] - m[t][e]);
+          w[e] = ex2(lv[t][e] - mv[t][e]);
+          w[2 + e] = ex2(lv[t][2 + e] - mv[t][e]);
         }
-        uint32_t pb[NT][2];
+        pb[t][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+        pb[t][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+      }
+      // ---- O^T += V^T P^T ----------------------------------------------------
+      const uint8_t* vim = im + kv4::off_v(C) + gid * 4 * D + tig * D;
+      // (bytes of rows never written may be anything: kept finite, their weight is 0)
+      const uint32_t vs = 0x7f7f7f7fu & *reinterpret_cast<const uint32_t*>(
+          im + kv4::off_vs(C) + (C == 128 ? gid : gid >> 1) * 16 + 4 * tig);
+      const ScalePair s0 = scale_pair(vs, 0x4140, k16), s1 = scale_pair(vs, 0x4342, k16);
+      uint32_t x0[D / 4], x1[D / 4];
+      if constexpr (C == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vim);
+        const uint4 y = *reinterpret_cast<const uint4*>(vim + 32 * D);
+        x0[0] = x.x; x0[1] = x.y; x0[2] = x.z; x0[3] = x.w;
+        x1[0] = y.x; x1[1] = y.y; x1[2] = y.z; x1[3] = y.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(vim);
+        const uint2 y = *reinterpret_cast<const uint2*>(vim + 32 * D);
+        x0[0] = x.x; x0[1] = x.y;
+        x1[0] = y.x; x1[1] = y.y;
+      }
+#pragma unroll
+      for (int w = 0; w < D / 4; ++w) {
+        uint32_t a0[4], a1[4];
+        widen4(x0[w], s0, k16, a0);
+        widen4(x1[w], s1, k16, a1);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mr = m[t][e] == kNegInf ? 0.f : m[t][e];
-            p[e] = ex2(sc[t][e] - mr);
-            p[2 + e] = ex2(sc[t][2 + e] - mr);
-            l[t][e] += p[e] + p[2 + e];
-          }
-          // weights times the rows' exponents, rounded to the operand's bf16
-          // (the sum keeps the unrounded weights)
-          pb[t][0] = transpose8x8(pack_bf16x2(p[0] * wa, p[1] * wa));
-          pb[t][1] = transpose8x8(pack_bf16x2(p[2] * wb, p[3] * wb));
-        }
-        // ---- O^T += V^T P^T ----------------------------------------------------
-        const uint8_t* vim = im + kv4::off_v(C) + gid * 4 * D + tig * D;
-        const uint32_t vs = *reinterpret_cast<const uint32_t*>(
-            im + kv4::off_vs(C) + (C == 128 ? gid : gid >> 1) * 16 + 4 * tig);
-        const ScalePair s0 = scale_pair(vs, 0x4140), s1 = scale_pair(vs, 0x4342);
-        uint32_t x0[D / 4], x1[D / 4];
-        if constexpr (C == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vim);
-          const uint4 y = *reinterpret_cast<const uint4*>(vim + 32 * D);
-          x0[0] = x.x; x0[1] = x.y; x0[2] = x.z; x0[3] = x.w;
-          x1[0] = y.x; x1[1] = y.y; x1[2] = y.z; x1[3] = y.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vim);
-          const uint2 y = *reinterpret_cast<const uint2*>(vim + 32 * D);
-          x0[0] = x.x; x0[1] = x.y;
-          x1[0] = y.x; x1[1] = y.y;
-        }
-#pragma unroll
-        for (int w = 0; w < D / 4; ++w) {
-          const uint32_t a0 = widen<0>(x0[w], s0), a1 = widen<1>(x0[w], s0);
-          const uint32_t a2 = widen<0>(x1[w], s1), a3 = widen<1>(x1[w], s1);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_16816(o[t][2 * w], a0, a1, a2, a3, pb[t][0], pb[t][1]);
-          const uint32_t c0 = widen<2>(x0[w], s0), c1 = widen<3>(x0[w], s0);
-          const uint32_t c2 = widen<2>(x1[w], s1), c3 = widen<3>(x1[w], s1);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma_16816(o[t][2 * w + 1], c0, c1, c2, c3, pb[t][0], pb[t][1]);
+          mma_16816(o[t][2 * w], a0[0], a0[1], a1[0], a1[1], pb[t][0], pb[t][1]);
+          mma_16816(o[t][2 * w + 1], a0[2], a0[3], a1[2], a1[3], pb[t][0], pb[t][1]);
         }
       }
+    };
+
+    for (; at.s < at.nu && u < units; ++at.s, ++u) {
+      const int st = u % F::kStages;
+      mbar_wait(&full[st], (uint32_t)((u / F::kStages) & 1), a.err);
+      const int t0 = meta[st];
+      if (t0 >= 0) image(ring + st * F::kTB, t0);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      issue(u + F::kStages, st);
     }
-    const bool ends = s == nu;
-    if (ends) next_segment();
+    const bool ends = at.s == at.nu;
+    if (ends) next_segment(at);
 
     // ---- merge the eight warps ---------------------------------------------------
 #pragma unroll
@@ -448,29 +567,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         const int hl = 8 * t + 2 * tig + e;
-        if (gid == 0) ml[warp * F::kHeads + hl] = make_float2(m[t][e], x);
+        if (gid == 0) ml[warp * F::kHeads + hl] = make_float4(m[t][e], x, mv[t][e], 0.f);
         float* row = merge + (warp * F::kHeads + hl) * F::kLd + gid * D;
 #pragma unroll
         for (int k = 0; k < MT; ++k)
           *reinterpret_cast<float2*>(row + 2 * k) = make_float2(o[t][k][e], o[t][k][2 + e]);
       }
-    named_bar_or(1, kConsThreads, false);
+    named_bar_or(1, kThreads, false);
     const bool direct = starts && ends;
     float* slot = a.ws + ((int64_t)blockIdx.x * 2 + (at_first ? 0 : 1)) * F::kSlot;
-    for (int e = threadIdx.x; e < F::kHeads * (C / 4); e += kConsThreads) {
+    for (int e = threadIdx.x; e < F::kHeads * (C / 4); e += kThreads) {
       const int hl = e / (C / 4), d = (e % (C / 4)) * 4;
-      float M = kNegInf;
+      float M = kNone, MV = kNone;
 #pragma unroll
-      for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, ml[w * F::kHeads + hl].x);
-      const float mr = M == kNegInf ? 0.f : M;
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, ml[w * F::kHeads + hl].x);
+        MV = fmaxf(MV, ml[w * F::kHeads + hl].z);
+      }
       float L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kConsWarps; ++w) {
-        const float2 x = ml[w * F::kHeads + hl];
-        const float f = ex2(x.x - mr);
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = ml[w * F::kHeads + hl];
+        const float f = ex2(x.z - MV);
         const float4 y = *reinterpret_cast<const float4*>(merge + (w * F::kHeads + hl) * F::kLd + d);
-        L = fmaf(x.y, f, L);
+        L = fmaf(x.y, ex2(x.x - M), L);
         acc.x = fmaf(y.x, f, acc.x);
         acc.y = fmaf(y.y, f, acc.y);
         acc.z = fmaf(y.z, f, acc.z);
@@ -479,8 +600,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
       if (direct) {
         if (h0 + hl < a.group) {
           const int head = kvh * a.group + h0 + hl;
-          const float den = L + (a.sink != nullptr && M != kNegInf ? ex2(a.sink[head] * kLog2e - M) : 0.f);
-          const float inv = den == 0.f ? 0.f : 1.f / den;
+          const float inv = out_factor(M, L, MV, a.sink, head);
           uint2 w;
           w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
           w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
@@ -488,12 +608,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
         }
       } else {
         *reinterpret_cast<float4*>(slot + hl * C + d) = acc;
-        if (d == 0) *reinterpret_cast<float2*>(slot + F::kHeads * C + 2 * hl) = make_float2(M, L);
+        if (d == 0) *reinterpret_cast<float4*>(slot + F::kHeads * C + 4 * hl) = make_float4(M, L, MV, 0.f);
       }
     }
-    named_bar_or(1, kConsThreads, false);
-    (void)cur_hv;
+    named_bar_or(1, kThreads, false);
   }
+  // after a wait that gave up, copies may still be on their way in
+  for (int u = max(0, units - F::kStages); u < units; ++u)
+    mbar_wait(&full[u % F::kStages], (uint32_t)((u / F::kStages) & 1), a.err, false);
 }
 
 // One block per (sequence, head tile): merges the pieces that lie in more
@@ -509,7 +631,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long before = 0, all = 0;
   for (int i = threadIdx.x; i < a.batch; i += 256) {
-    const int u = units_of(seen_of(a, a.pos[i]));
+    const int u = units_of(seen_of(a, clip_pos(a.pos[i])));
     all += u;
     if (i < b) before += u;
   }
@@ -529,7 +651,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
     before += part[0][w];
     all += part[1][w];
   }
-  const int nu = units_of(seen_of(a, a.pos[b]));
+  const int nu = units_of(seen_of(a, clip_pos(a.pos[b])));
   const int64_t U = (int64_t)all * HV;
   const int G = (int)min((int64_t)grid, U);
   const int64_t u0 = (int64_t)before * HV + (int64_t)hv * nu, u1 = u0 + nu;
@@ -539,26 +661,27 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
     const int hl = e / (C / 4), d = (e % (C / 4)) * 4;
     if (h0 + hl >= a.group) continue;
     const int head = kvh * a.group + h0 + hl;
-    float M = kNegInf, L = 0.f;
+    float M = kNone, L = 0.f, MV = kNone;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nu > 0) {
       for (int i = i0; i <= i1; ++i) {
         const int which = i > i0 || cta_first(U, G, i) == u0 ? 0 : 1;
         const float* slot = a.ws + ((int64_t)i * 2 + which) * F::kSlot;
-        const float2 x = *reinterpret_cast<const float2*>(slot + F::kHeads * C + 2 * hl);
+        const float4 x = *reinterpret_cast<const float4*>(slot + F::kHeads * C + 4 * hl);
         const float4 y = *reinterpret_cast<const float4*>(slot + hl * C + d);
-        const float mn = fmaxf(M, x.x), mr = mn == kNegInf ? 0.f : mn;
-        const float f0 = ex2(M - mr), f1 = ex2(x.x - mr);
+        const float mn = fmaxf(M, x.x);
+        L = L * ex2(M - mn) + x.y * ex2(x.x - mn);
         M = mn;
-        L = L * f0 + x.y * f1;
+        const float vn = fmaxf(MV, x.z);
+        const float f0 = ex2(MV - vn), f1 = ex2(x.z - vn);
+        MV = vn;
         acc.x = acc.x * f0 + y.x * f1;
         acc.y = acc.y * f0 + y.y * f1;
         acc.z = acc.z * f0 + y.z * f1;
         acc.w = acc.w * f0 + y.w * f1;
       }
     }
-    const float den = L + (a.sink != nullptr && M != kNegInf ? ex2(a.sink[head] * kLog2e - M) : 0.f);
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float inv = out_factor(M, L, MV, a.sink, head);
     uint2 w;
     w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
     w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
@@ -597,7 +720,7 @@ extern "C" {
 size_t csa_kv4_decode_workspace(int nh, int nkv, int c) {
   if (nkv < 1 || nh < nkv || nh % nkv != 0 || (c != 64 && c != 128)) return 0;
   const int group = nh / nkv, heads = 8 * dec_nt(group);
-  return (size_t)dec_grid(group) * 2 * (heads * c + 2 * heads) * 4;
+  return (size_t)dec_grid(group) * 2 * (heads * c + 4 * heads) * 4;
 }
 
 csa_status csa_kv4_decode_attn(const csa_kv4_cache* cache, const int64_t* pos, const void* q,
@@ -610,6 +733,8 @@ csa_status csa_kv4_decode_attn(const csa_kv4_cache* cache, const int64_t* pos, c
   API_REQUIRE(first >= 0, "first must be >= 0");
   API_REQUIRE(scale == scale && scale > -3.4e38f && scale < 3.4e38f, "scale must be finite");
   API_SUPPORTED(nh <= 65536, "csa_kv4_decode_attn needs nh <= 65536");
+  API_SUPPORTED(cache->num_blocks * cache->nkv <= INT_MAX / (cache->block_tokens / 16),
+                "csa_kv4_decode_attn needs a pool of fewer than 2^31 / 16 tokens and heads");
   API_SUPPORTED((cache->max_blocks * cache->block_tokens / 128 + 2) * cache->batch < ((int64_t)1 << 31) &&
                     (int64_t)cache->batch * nh < ((int64_t)1 << 31),
                 "csa_kv4_decode_attn: the batch has too many tokens");
@@ -635,9 +760,10 @@ csa_status csa_kv4_decode_attn(const csa_kv4_cache* cache, const int64_t* pos, c
   a.err = flag;
   a.max_blocks = cache->max_blocks;
   a.num_blocks = cache->num_blocks;
-  a.capacity = cache->max_blocks * cache->block_tokens;
-  a.window = window;
-  a.first = first;
+  // (2^31 tokens at most; positions end one short of that)
+  a.capacity = (int)std::min<int64_t>(cache->max_blocks * cache->block_tokens, INT_MAX);
+  a.window = (int)std::min<int64_t>(window, INT_MAX);
+  a.first = (int)std::min<int64_t>(first, INT_MAX);
   a.batch = (int)cache->batch;
   a.nkv = cache->nkv;
   a.nh = nh;

@@ -166,35 +166,43 @@ def kv4_store(cache, table, pos, k, v, count=None):
 
 
 def kv4_rows(cache, table, b, h, us, c):
-    """K, V [m, c] of the positions us that are there, and which those are."""
-    ks, vs, have = [], [], []
+    """K, V [m, c] of the positions us that are there, and r of the V rows."""
+    ks, vs, rs = [], [], []
     for u in us:
         img = kv4_image(cache, table, b, h, int(u))
-        have.append(img is not None)
         if img is not None:
-            ks.append(read_row(img, int(u) % 16, c, False))
-            vs.append(read_row(img, int(u) % 16, c, True))
-    return np.array(ks).reshape(-1, c), np.array(vs).reshape(-1, c), np.array(have, bool)
+            t = int(u) % 16
+            ks.append(read_row(img, t, c, False))
+            vs.append(read_row(img, t, c, True))
+            rs.append(2.0 ** (int(img[18 * c + 2 * (8 * ((t >> 1) & 1) + 2 * (t >> 2) + (t & 1)) + 1]) - 127))
+    return np.array(ks).reshape(-1, c), np.array(vs).reshape(-1, c), np.array(rs)
 
 
 def kv4_decode(q, cache, table, pos, scale, window, first, sink):
-    """q [B, nh, c] -> (out, spread, reach) as window_attn."""
+    """q [B, nh, c] -> (out, spread, reach) as window_attn, the largest
+    max|q| * sum|k| per head, and max_u(p_u r_u) * sum_u |v_u| / r_u."""
     q = np.asarray(q, np.float64)
     B, nh, c = q.shape
     nkv = cache.shape[1]
     g = nh // nkv
-    out, reach = np.zeros(q.shape), np.zeros((B, nh, 1))
-    spread = np.zeros(q.shape)
+    out, reach, far = np.zeros(q.shape), np.zeros((B, nh, 1)), np.zeros((B, nh, 1))
+    spread, under = np.zeros(q.shape), np.zeros(q.shape)
     for b in range(B):
         if pos[b] < 0:
             continue
         us = visible(int(pos[b]), window, first)
         for h in range(nkv):
-            k, v, _ = kv4_rows(cache, table, b, h, us, c)
+            k, v, r = kv4_rows(cache, table, b, h, us, c)
             for x in range(h * g, (h + 1) * g):
                 out[b, x], spread[b, x], reach[b, x] = attend(
                     q[b, x], k, v, scale, None if sink is None else float(sink[x]))
-    return out, spread, reach
+                if len(k):
+                    far[b, x] = np.abs(q[b, x]).max() * np.abs(k).sum(1).max()
+                    l = scale * (k @ q[b, x])
+                    p = np.exp(l - l.max())
+                    p /= p.sum() + (0.0 if sink is None else np.exp(float(sink[x]) - l.max()))
+                    under[b, x] = (p * r).max() * (np.abs(v) / r[:, None]).sum(0)
+    return out, spread, reach, far, under
 
 
 # --------------------------------------------------------------- block tables ---

@@ -30,6 +30,22 @@ def attn_bound(ref, spread, reach, scale, c, n, dt=torch.bfloat16):
     return HALF[dt] * first + rel * spread + 1e-30
 
 
+def decode_bound(ref, spread, reach, far, under, scale, c, n):
+    """As attn_bound for the 4-bit cache's attention: its weights are f16 (a
+    half step of 2^-11), formed as 2^(logit + exponent - reference) in fp32
+    from numbers up to |logit| + 512 (a rounding each of the sum and the
+    difference), and query elements far below a head's largest keep 2^-25 of
+    it.  A weight p r below 2^-14 of the largest is an f16 subnormal: it is off
+    by up to half a subnormal step, 2^-25, in units of the reference, which is
+    at most the largest p r; times |v| / r, summed over the rows, that is
+    2^-25 under."""
+    d = 2 * abs(scale) * ((c + 6) * 2.0 ** -24 * reach + 2.0 ** -25 * far)
+    logit = 1.45 * abs(scale) * reach + 512
+    rel = np.expm1(2 * d) + 2.0 ** -21 + 2 * (n + 16) * 2.0 ** -24 + 2.0 ** -11 + 2 * logit * 2.0 ** -24
+    off = rel * spread + 2.0 ** -25 * under
+    return 2.0 ** -8 * (np.abs(ref) + off) + off + 1e-30
+
+
 def check(got, ref, bound, what=""):
     g = f64(got) if torch.is_tensor(got) else got
     assert g.shape == ref.shape, (what, g.shape, ref.shape)
@@ -65,4 +81,4 @@ def filled_cache(rng, pool, nkv, c, block_tokens):
     return cache
 
 
-__all__ = ["S", "HALF", "f64", "attn_bound", "check", "random_table", "filled_cache", "np", "torch"]
+__all__ = ["S", "HALF", "f64", "attn_bound", "decode_bound", "check", "random_table", "filled_cache", "np", "torch"]

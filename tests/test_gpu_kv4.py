@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import compressed_sparse_attention_11_b200 as csa
-from _serving import S, attn_bound, check, f64, filled_cache, random_table
+from _serving import S, check, decode_bound, f64, filled_cache, random_table
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -124,8 +124,8 @@ def decode_case(c, nkv, g, P, lens, W, first, sink, seed, scale=None):
     scale = c ** -0.5 if scale is None else scale
     out = csa.csa_kv4_decode_attn(q.to(DEV), dev(cache), dev(table), torch.tensor(pos, device=DEV),
                                   scale, W, first, None if z is None else dev(z))
-    ref, spread, reach = S.kv4_decode(f64(q), cache, table, pos, scale, W, first, z)
-    check(out, ref, attn_bound(ref, spread, reach, scale, c, max(max(lens), 1)), "decode")
+    ref, spread, reach, far, under = S.kv4_decode(f64(q), cache, table, pos, scale, W, first, z)
+    check(out, ref, decode_bound(ref, spread, reach, far, under, scale, c, max(max(lens), 1)), "decode")
     csa.csa_check()
 
 
@@ -148,11 +148,73 @@ def test_decode_matches_definition(c, nkv, g, P, lens, W, first, sink):
     decode_case(c, nkv, g, P, lens, W, first, sink, seed=sum(lens) + c)
 
 
+@pytest.mark.parametrize("c,nkv,g,lens,W,first", [(128, 8, 8, [9000, 300, 12000, 5, 7777] * 4, 0, 0),
+                                                  (64, 8, 16, [16000, 130, 9001] * 6, 0, 0),
+                                                  (128, 8, 4, [20000, 19999, 150] * 8, 3000, 40)])
+def test_decode_long_shares(c, nkv, g, lens, W, first):
+    """Enough work that every CTA streams many units and several sequences."""
+    P, B = 128, len(lens)
+    rng = np.random.default_rng(B)
+    table, pool = random_table(rng, lens, P, -(-max(lens) // P))
+    cache = csa.csa_kv4_cache(pool, nkv, c, P)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    cache[..., :16 * c] = torch.randint(17, 256, cache[..., :16 * c].shape, generator=gen, device=DEV, dtype=torch.uint8)
+    cache[..., 16 * c:18 * c] = torch.randint(30, 70, cache[..., 16 * c:18 * c].shape, generator=gen, device=DEV,
+                                              dtype=torch.uint8)
+    cache[..., 18 * c:] = torch.randint(122, 126, cache[..., 18 * c:].shape, generator=gen, device=DEV, dtype=torch.uint8)
+    q = torch.randn((B, nkv * g, c), generator=gen, device=DEV).bfloat16()
+    pos = torch.tensor(lens, device=DEV) - 1
+    out = csa.csa_kv4_decode_attn(q, cache, dev(table), pos, c ** -0.5, W, first)
+    csa.csa_check()
+    for b in (0, 1, B - 2, B - 1):      # the rows fetched, then plain fp64 on the device
+        k, v = (x[0].double() for x in csa.csa_kv4_fetch(cache, dev(table[b:b + 1]), torch.zeros(1, dtype=torch.int64,
+                                                                                              device=DEV),
+                                                         lens[b], dtype=torch.float32))
+        u = torch.arange(lens[b], device=DEV)
+        u = u[(u >= lens[b] - W) | (u < first)] if W else u
+        kk, vv = (x[u].repeat_interleave(g, 1).transpose(0, 1) for x in (k, v))
+        l = torch.einsum("hd,hud->hu", q[b].double(), kk) * c ** -0.5
+        p = torch.softmax(l, 1)
+        ref, spread = (torch.einsum("hu,hud->hd", p, x) for x in (vv, vv.abs()))
+        reach = torch.einsum("hd,hud->hu", q[b].double().abs(), kk.abs()).amax(1, keepdim=True)
+        far = q[b].double().abs().amax(1, keepdim=True) * kk.abs().sum(2).amax(1, keepdim=True)
+        # value exponents within 2^4 of one another: r_u / r_w <= 16
+        under = 16 * p.amax(1, keepdim=True) * vv.abs().sum(1)
+        check(out[b], f64(ref), decode_bound(*[f64(x) for x in (ref, spread, reach, far, under)], c ** -0.5, c,
+                                             len(u)), f"b={b}")
+
+
 def test_decode_many_sequences_and_large_logits():
     decode_case(64, 2, 2, 16, [(37 * i) % 90 for i in range(70)], 0, 0, True, seed=3)
     decode_case(128, 1, 8, 16, [400], 0, 0, False, seed=4, scale=3.0)      # nearly one-hot weights
     decode_case(128, 1, 8, 16, [400], 0, 0, True, seed=5, scale=0.0)
     decode_case(128, 1, 8, 16, [400], 0, 0, True, seed=6, scale=-0.2)
+
+
+@pytest.mark.parametrize("c", [64, 128])
+def test_decode_rows_of_very_different_size(c):
+    """Value rows from 2^-40 to 2^40, the largest with weights near 0, and query
+    heads of every size (one of zeros): no row drowns another."""
+    rng = np.random.default_rng(31)
+    n, nkv, g, P = 300, 2, 4, 32
+    table, pool = random_table(rng, [n], P, 10)
+    cache = filled_cache(rng, pool, nkv, c, P)
+    cache[..., 18 * c + 1::2] = rng.integers(87, 160, cache[..., 18 * c + 1::2].shape)   # value exponents
+    for h in range(nkv):       # keys that hide the largest values' rows: the query below is positive
+        for u in range(n):
+            img = S.kv4_image(cache, table, 0, h, u)
+            E = img[18 * c + 2 * (8 * ((u >> 1) & 1) + 2 * (u >> 2 & 3) + (u & 1)) + 1]
+            if E > 127:
+                S.write_row(img, u % 16, c, False, np.full(c, -7), np.full(c // 16, 56), int(127 + (E - 127) // 16))
+    q = np.abs(rng.standard_normal((1, nkv * g, c))) * 2.0 ** np.array([-100, -20, 0, 3, 60, 126, -140, 0])[None, :, None]
+    q[0, 7] = 0
+    q = torch.from_numpy(q).bfloat16()
+    for scale in (0.05, 1e-30):
+        out = csa.csa_kv4_decode_attn(q.to(DEV), dev(cache), dev(table), torch.tensor([n - 1], device=DEV), scale)
+        ref, spread, reach, far, under = S.kv4_decode(f64(q), cache, table, [n - 1], scale, 0, 0, None)
+        fine = [h for h in range(nkv * g) if np.abs(scale * reach[0, h]) < 1e4]
+        assert len(fine) >= 5
+        check(out[:, fine], ref[:, fine], decode_bound(ref, spread, reach, far, under, scale, c, n)[:, fine], str(scale))
 
 
 def test_decode_hidden_rows_do_not_leak():
@@ -170,8 +232,8 @@ def test_decode_hidden_rows_do_not_leak():
     q = torch.from_numpy(rng.standard_normal((1, 4, c))).bfloat16()
     out = csa.csa_kv4_decode_attn(q.to(DEV), dev(cache), dev(table), torch.tensor([n - 1], device=DEV),
                                   0.1, W, first)
-    ref, spread, reach = S.kv4_decode(f64(q), cache, table, [n - 1], 0.1, W, first, None)
-    check(out, ref, attn_bound(ref, spread, reach, 0.1, c, n), "hidden")
+    ref, spread, reach, far, under = S.kv4_decode(f64(q), cache, table, [n - 1], 0.1, W, first, None)
+    check(out, ref, decode_bound(ref, spread, reach, far, under, 0.1, c, n), "hidden")
     # one that is seen makes its heads NaN
     S.write_row(S.kv4_image(cache, table, 0, 0, n - 1), (n - 1) % 16, c, True, np.zeros(c, int), np.zeros(8, int), 255)
     out = csa.csa_kv4_decode_attn(q.to(DEV), dev(cache), dev(table), torch.tensor([n - 1], device=DEV),
@@ -188,8 +250,8 @@ def test_decode_positions_beyond_the_table_and_before_the_start():
     for pos, W, first in (([100, -1], 0, 0), ([100, -7], 50, 3), ([500, 63], 20, 0)):
         out = csa.csa_kv4_decode_attn(q.to(DEV), dev(cache), dev(table), torch.tensor(pos, device=DEV), 0.125,
                                       W, first)
-        ref, spread, reach = S.kv4_decode(f64(q), cache, table, pos, 0.125, W, first, None)
-        check(out, ref, attn_bound(ref, spread, reach, 0.125, c, 64), str(pos))
+        ref, spread, reach, far, under = S.kv4_decode(f64(q), cache, table, pos, 0.125, W, first, None)
+        check(out, ref, decode_bound(ref, spread, reach, far, under, 0.125, c, 64), str(pos))
 
 
 def test_offsets_past_32_bits():

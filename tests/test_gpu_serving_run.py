@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import compressed_sparse_attention_11_b200 as csa
-from _serving import S, attn_bound, check, f64
+from _serving import S, attn_bound, check, decode_bound, f64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -79,9 +79,9 @@ def test_prompt_fork_decode_free_compact(c, P, W, first):
         csa.csa_kv4_decode_attn(qo[:, 0], cache, table, at, scale, W, first, z, ws=ws, out=o)
 
     def held(what):
-        ref, spread, reach = S.kv4_decode(f64(qo[:, 0]), cache.cpu().numpy(), table.cpu().numpy(), at.tolist(), scale,
-                                          W, first, f64(z))
-        check(o, ref, attn_bound(ref, spread, reach, scale, c, n + 8), what)
+        ref, spread, reach, far, under = S.kv4_decode(f64(qo[:, 0]), cache.cpu().numpy(), table.cpu().numpy(), at.tolist(),
+                                               scale, W, first, f64(z))
+        check(o, ref, decode_bound(ref, spread, reach, far, under, scale, c, n + 8), what)
 
     step()
     held("first step")
