@@ -14,9 +14,10 @@
 // and a nibble becomes an operand where it stands: in a 16-bit word of four,
 // (x & 0x00f0) | 0x5400 is the f16 64 + n and one fma with (s, -72 s) gives
 // s (n - 8) exactly; (x & 0x000f) | 0x6400 is 1024 + n and takes a subtraction
-// and a product; the upper two follow after one shift.  Logic and shifts run
-// at half the rate of the fmas here, and were the bound with bf16 operands,
-// whose seven mantissa bits want a shift per nibble.
+// and a product; the upper two follow after one shift.  Logic and shifts were
+// the bound with bf16 operands, whose seven mantissa bits want a shift per
+// nibble; now these and the f16 arithmetic weigh about the same (190 us of
+// instructions where the bytes take 148).
 // f16's range: a query head is scaled to largest element 1 .. 2 (elements below
 // 2^-14 of it keep an absolute 2^-25), and the second product's weight is
 // w_u = 2^(l_u + E_u - M'), E_u the value row's exponent and M' a running
@@ -27,15 +28,18 @@
 // than an SM's share of HBM time allows; mma.sync takes them from registers.
 //
 // Work: units of 8 images (128 tokens) of one (sequence, head tile), in one
-// flat list that is cut evenly over the CTAs whatever the lengths.  Warp w of
-// 8 takes image w of each unit, brought in by bulk copies through a ring of
-// its own, so no warp waits for another (with one ring for the CTA the warps
-// moved in step: 302 us where this takes XX, 32 sequences of 16-32 K tokens,
-// 64 / 8 heads x 128), with its own running maxima, sum and output; the eight
-// are merged where a sequence ends or the CTA's share does.  What a CTA covers
-// whole is written out; other pieces go to the workspace (two slots a CTA) and
-// a second kernel merges them.
+// flat list that is cut evenly over the CTAs whatever the lengths.  Warp w of 4
+// takes images 2 w and 2 w + 1 of each unit, brought in by bulk copies through
+// a ring of its own, so no warp waits for another (one ring for the CTA moved
+// the warps in step and took a fifth longer), with its own running maxima, sum
+// and output; the four are merged where a sequence ends or the CTA's share
+// does (four CTAs of four warps on an SM: 197 us; two of eight: 201; times at
+// 32 sequences of 16-32 K tokens, 64 / 8 heads x 128, whose bytes alone take
+// 148).  What a CTA covers whole is written out; other pieces go to the
+// workspace (two slots a CTA) and a second kernel merges them.
 #include <limits.h>
+
+#include <type_traits>
 
 #include "api_check.h"
 #include "common.cuh"
@@ -49,9 +53,10 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnitTiles = kWarps;  // images per unit
+constexpr int kPair = 2;                     // neighbouring images a warp takes at once
+constexpr int kUnitTiles = kPair * kWarps;  // images per unit
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kNone = -3e38f;  // running maximum of a head that has seen nothing
 
@@ -158,14 +163,22 @@ __device__ __forceinline__ ScalePair scale_pair(uint32_t bytes, uint32_t sel, co
   p.n72 = mul_f16x2(p.s, k.m72);
   return p;
 }
+// (w & kMask) | k in one instruction (left to itself the compiler took two,
+// and the kernel 229 us instead of 201).
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t k) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(kMask), "r"(k));
+  return d;
+}
 // Nibbles j and j + 4 of w, j = 0 .. 3 -> s (n - 8) 2^-8 in the two halves.
 __device__ __forceinline__ void widen4(uint32_t w, const ScalePair& s, const Bases& k,
                                        uint32_t (&v)[4]) {
   const uint32_t y = w >> 8;
-  v[0] = mul_f16x2(add_f16x2((w & 0x000f000fu) | k.k1024, k.m1032), s.s);
-  v[1] = fma_f16x2((w & 0x00f000f0u) | k.k64, s.s, s.n72);
-  v[2] = mul_f16x2(add_f16x2((y & 0x000f000fu) | k.k1024, k.m1032), s.s);
-  v[3] = fma_f16x2((y & 0x00f000f0u) | k.k64, s.s, s.n72);
+  v[0] = mul_f16x2(add_f16x2(and_or<0x000f000fu>(w, k.k1024), k.m1032), s.s);
+  v[1] = fma_f16x2(and_or<0x00f000f0u>(w, k.k64), s.s, s.n72);
+  v[2] = mul_f16x2(add_f16x2(and_or<0x000f000fu>(y, k.k1024), k.m1032), s.s);
+  v[3] = fma_f16x2(and_or<0x00f000f0u>(y, k.k64), s.s, s.n72);
 }
 
 // A piece's state per head: running maximum M of the logits (log2 units), sum
@@ -179,20 +192,21 @@ __device__ __forceinline__ float out_factor(float M, float L, float MV, const fl
 template <int C, int NT>
 struct Cfg {
   static constexpr int kTB = kv4::tile_bytes(C);
-  static constexpr int kStages = 4;  // images in a warp's ring
+  static constexpr int kStages = 2;  // image pairs in a warp's ring
+  static constexpr int kStageBytes = kPair * kTB;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kLd = C + 4;  // padded row of the merge buffer (floats)
   static constexpr int kSlot = kHeads * C + 4 * kHeads;  // floats of a workspace slot
-  static constexpr int off_merge() { return kWarps * kStages * kTB; }
+  static constexpr int off_merge() { return kWarps * kStages * kStageBytes; }
   static constexpr int off_ml() { return off_merge() + kWarps * kHeads * kLd * 4; }
   static constexpr int off_meta() { return off_ml() + kWarps * kHeads * 16; }
-  static constexpr int off_bar() { return off_meta() + kWarps * kStages * 4; }
+  static constexpr int off_bar() { return off_meta() + kWarps * kStages * kPair * 4; }
   static constexpr int off_list() { return off_bar() + kWarps * kStages * 8 + 64; }
   static size_t smem(int batch) { return off_list() + (size_t)(2 * batch + 1) * 4; }
 };
 
 template <int C, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(const __grid_constant__ DecArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(const __grid_constant__ DecArgs a) {
   using F = Cfg<C, NT>;
   constexpr int D = C / 8;    // dims of a V chunk
   constexpr int KS = C / 16;  // k-steps of Q.K
@@ -201,15 +215,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
   float* merge = reinterpret_cast<float*>(smem + F::off_merge());
   float4* ml = reinterpret_cast<float4*>(smem + F::off_ml());  // (M, L, MV, -)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + warp * F::kStages * F::kTB;
-  int* meta = reinterpret_cast<int*>(smem + F::off_meta()) + warp * F::kStages;  // first token, or -1
+  uint8_t* ring = smem + warp * F::kStages * F::kStageBytes;
+  int2* meta = reinterpret_cast<int2*>(smem + F::off_meta()) + warp * F::kStages;  // first tokens, or -1
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::off_bar()) + warp * F::kStages;
   int* scan = reinterpret_cast<int*>(smem + F::off_bar() + kWarps * F::kStages * 8);
   int* first_unit = reinterpret_cast<int*>(smem + F::off_list());  // [batch + 1]
   int* position = first_unit + a.batch + 1;                         // [batch]
 
   if (lane == 0) {
-    for (int i = 0; i < F::kStages; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < F::kStages; ++i) mbar_init(&full[i], kPair);
     fence_mbar_init();
   }
   __syncwarp();
@@ -287,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
   }
   const int units = (int)min(u_hi - u_lo, (int64_t)INT_MAX);
 
-  // ---- this warp's images, looked up 32 units at a time: lane i those of
-  // unit base + i (the block numbers are on their way until they are used) ----
+  // ---- this warp's images, looked up 16 units at a time: lane 2 i + k image
+  // k of unit base + i (the block numbers are on their way until they are used)
   Place look = at;  // the first unit of the batch to come
   int look_unit = 0;
   int t0_c = -1, img_c = 0;                  // this batch: first token (-1: none), image number
@@ -299,15 +313,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
     tile_n = -1;
     if (look_unit >= units) return;
     Place p = look;
-    if (look_unit + lane < units) {
-      p.s += lane;
+    if (look_unit + (lane >> 1) < units) {
+      p.s += lane >> 1;
       while (p.s >= p.nu) {
         const int rest = p.s - p.nu;
         next_segment(p);
         p.s = rest;
       }
       const Seen v = seen_of(a, position[p.b]);
-      const int i = p.s * kUnitTiles + warp;
+      const int i = p.s * kUnitTiles + 2 * warp + (lane & 1);
       if (i < v.images) {
         tile_n = i < v.head ? i : v.tail + (i - v.head);
         const int j = tile_n / a.tiles_per_block;
@@ -315,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
         blk_n = __ldg(a.table + p.b * a.max_blocks + j);
       }
     }
-    look_unit += 32;
+    look_unit += 16;
     if (look_unit < units) {
-      look.s += 32;
+      look.s += 16;
       while (look.s >= look.nu) {
         const int rest = look.s - look.nu;
         next_segment(look);
@@ -325,16 +339,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
       }
     }
   };
-  auto issue = [&](int u, int st) {  // the image of unit u into its stage, which is free
+  auto issue = [&](int u, int st) {  // the images of unit u into their stage, which is free
     if (u >= units) return;
-    if ((u & 31) == 0 && u > 0) look_up();
-    const int t0 = __shfl_sync(0xffffffffu, t0_c, u & 31);
-    const int img = __shfl_sync(0xffffffffu, img_c, u & 31);
-    if (lane == 0) {
-      meta[st] = t0;
+    if ((u & 15) == 0 && u > 0) look_up();
+    const int from = 2 * (u & 15) + (lane & 1);
+    const int t0 = __shfl_sync(0xffffffffu, t0_c, from);
+    const int img = __shfl_sync(0xffffffffu, img_c, from);
+    if (lane < 2) {
+      reinterpret_cast<int*>(&meta[st])[lane] = t0;
       if (t0 >= 0) {
         mbar_arrive_expect_tx(&full[st], F::kTB);
-        bulk_load(ring + st * F::kTB, a.cache + (int64_t)img * F::kTB, F::kTB, &full[st]);
+        bulk_load(ring + st * F::kStageBytes + lane * F::kTB, a.cache + (int64_t)img * F::kTB,
+                  F::kTB, &full[st]);
       } else {
         mbar_arrive(&full[st]);
       }
@@ -406,83 +422,105 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
     }
 
     const Bases k16 = bases();
-    auto image = [&](const uint8_t* im, int t0) {
+    // Images 0 .. N - 1 of a stage, step by step for all of them, so that the
+    // chains of one hide under the other's.
+    auto images = [&](auto count, const uint8_t* im0, int t0a, int t0b) {
+      constexpr int N = decltype(count)::value;
+      const int t0[2] = {t0a, t0b};
+      float sc[N][NT][4];
+      uint32_t ex[N][2];
       // ---- S^T = K Q^T ----------------------------------------------------
-      float sc[NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
-      uint32_t ka[C / 32], kb[C / 32];
-      ScalePair sa[C / 64], sb[C / 64];
-      if constexpr (C == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(im + gid * 64 + tig * 16);
-        const uint4 y = *reinterpret_cast<const uint4*>(im + (gid + 8) * 64 + tig * 16);
-        ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
-        kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
-        const uint32_t p = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + gid * 8 + 2 * tig);
-        const uint32_t r = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + (gid + 8) * 8 + 2 * tig);
-        sa[0] = scale_pair(p, 0x4040, k16); sa[1] = scale_pair(p, 0x4141, k16);
-        sb[0] = scale_pair(r, 0x4040, k16); sb[1] = scale_pair(r, 0x4141, k16);
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(im + gid * 32 + tig * 8);
-        const uint2 y = *reinterpret_cast<const uint2*>(im + (gid + 8) * 32 + tig * 8);
-        ka[0] = x.x; ka[1] = x.y;
-        kb[0] = y.x; kb[1] = y.y;
-        sa[0] = scale_pair(im[kv4::off_ks(C) + gid * 4 + tig], 0x4040, k16);
-        sb[0] = scale_pair(im[kv4::off_ks(C) + (gid + 8) * 4 + tig], 0x4040, k16);
-      }
-      const uint32_t ea = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid);
-      const uint32_t eb = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid + 16);
+      for (int n = 0; n < N; ++n) {
+        const uint8_t* im = im0 + n * F::kTB;
 #pragma unroll
-      for (int w = 0; w < C / 32; ++w) {
-        uint32_t ra[4], rb[4];
-        widen4(ka[w], sa[w / 2], k16, ra);
-        widen4(kb[w], sb[w / 2], k16, rb);
+        for (int t = 0; t < NT; ++t) sc[n][t][0] = sc[n][t][1] = sc[n][t][2] = sc[n][t][3] = 0.f;
+        uint32_t ka[C / 32], kb[C / 32];
+        ScalePair sa[C / 64], sb[C / 64];
+        if constexpr (C == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(im + gid * 64 + tig * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(im + (gid + 8) * 64 + tig * 16);
+          ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
+          kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
+          const uint32_t p = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + gid * 8 + 2 * tig);
+          const uint32_t r = *reinterpret_cast<const uint16_t*>(im + kv4::off_ks(C) + (gid + 8) * 8 + 2 * tig);
+          sa[0] = scale_pair(p, 0x4040, k16); sa[1] = scale_pair(p, 0x4141, k16);
+          sb[0] = scale_pair(r, 0x4040, k16); sb[1] = scale_pair(r, 0x4141, k16);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(im + gid * 32 + tig * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(im + (gid + 8) * 32 + tig * 8);
+          ka[0] = x.x; ka[1] = x.y;
+          kb[0] = y.x; kb[1] = y.y;
+          sa[0] = scale_pair(im[kv4::off_ks(C) + gid * 4 + tig], 0x4040, k16);
+          sb[0] = scale_pair(im[kv4::off_ks(C) + (gid + 8) * 4 + tig], 0x4040, k16);
+        }
+        ex[n][0] = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid);
+        ex[n][1] = *reinterpret_cast<const uint16_t*>(im + kv4::off_exp(C) + 2 * gid + 16);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          mma_16816(sc[t], ra[0], rb[0], ra[1], rb[1], qf[t][2 * w][0], qf[t][2 * w][1]);
-          mma_16816(sc[t], ra[2], rb[2], ra[3], rb[3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+        for (int w = 0; w < C / 32; ++w) {
+          uint32_t ra[4], rb[4];
+          widen4(ka[w], sa[w / 2], k16, ra);
+          widen4(kb[w], sb[w / 2], k16, rb);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma_16816(sc[n][t], ra[0], rb[0], ra[1], rb[1], qf[t][2 * w][0], qf[t][2 * w][1]);
+            mma_16816(sc[n][t], ra[2], rb[2], ra[3], rb[3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+          }
         }
       }
       // ---- online softmax: l, and l + E of the value row ----------------------
-      const float ka_r = __uint_as_float((ea & 255u) << 23), kb_r = __uint_as_float((eb & 255u) << 23);
-      // E as a float; infinite for a row that is not finite (0 w then makes NaN)
-      const float va_e = ea >= 0xff00u ? __int_as_float(0x7f800000) : (float)(ea >> 8);
-      const float vb_e = eb >= 0xff00u ? __int_as_float(0x7f800000) : (float)(eb >> 8);
-      float lv[NT][4];
+      float lv[N][NT][4];
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // slots gid, gid + 8
+          const float kr = __uint_as_float((ex[n][r] & 255u) << 23);
+          // E as a float; infinite for a row that is not finite (0 w then makes NaN)
+          const float ve = ex[n][r] >= 0xff00u ? __int_as_float(0x7f800000) : (float)(ex[n][r] >> 8);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float2 s = mul2(mul2(make_float2(sc[n][t][2 * r], sc[n][t][2 * r + 1]), make_float2(kr, kr)),
+                                  make_float2(qfac[t][0], qfac[t][1]));
+            const float2 y = add2(s, make_float2(ve, ve));
+            sc[n][t][2 * r] = s.x;
+            sc[n][t][2 * r + 1] = s.y;
+            lv[n][t][2 * r] = y.x;
+            lv[n][t][2 * r + 1] = y.y;
+          }
+        }
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (t0[n] + 15 >= seen_n || (t0[n] < seen_lo && t0[n] + 15 >= seen_first)) {  // some row is hidden
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int u1 = t0[n] + tok_a + 2 * r;
+            if (!(u1 < seen_n && (u1 >= seen_lo || u1 < seen_first)))
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sc[n][t][2 * r + e] = lv[n][t][2 * r + e] = kNegInf;
+          }
+        }
+      float tm[NT][2], tv[NT][2];
       bool grow = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sc[t][e] = sc[t][e] * ka_r * qfac[t][e];
-          sc[t][2 + e] = sc[t][2 + e] * kb_r * qfac[t][e];
-          lv[t][e] = sc[t][e] + va_e;
-          lv[t][2 + e] = sc[t][2 + e] + vb_e;
-        }
-      if (t0 + 15 >= seen_n || (t0 < seen_lo && t0 + 15 >= seen_first)) {  // some row is hidden
-        const int ua = t0 + tok_a, ub = ua + 2;
-        const bool sa_ = ua < seen_n && (ua >= seen_lo || ua < seen_first);
-        const bool sb_ = ub < seen_n && (ub >= seen_lo || ub < seen_first);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (!sa_) sc[t][e] = lv[t][e] = kNegInf;
-            if (!sb_) sc[t][2 + e] = lv[t][2 + e] = kNegInf;
+          tm[t][e] = fmaxf(sc[0][t][e], sc[0][t][2 + e]);
+          tv[t][e] = fmaxf(lv[0][t][e], lv[0][t][2 + e]);
+          if (N > 1) {
+            tm[t][e] = fmaxf(tm[t][e], fmaxf(sc[N - 1][t][e], sc[N - 1][t][2 + e]));
+            tv[t][e] = fmaxf(tv[t][e], fmaxf(lv[N - 1][t][e], lv[N - 1][t][2 + e]));
           }
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          grow |= fmaxf(sc[t][e], sc[t][2 + e]) > m[t][e] + kRescaleLog2 ||
-                  fmaxf(lv[t][e], lv[t][2 + e]) > mv[t][e] + kRescaleLog2;
+          grow |= tm[t][e] > m[t][e] + kRescaleLog2 || tv[t][e] > mv[t][e] + kRescaleLog2;
+        }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(sc[t][e], sc[t][2 + e]), y = fmaxf(lv[t][e], lv[t][2 + e]);
+            float x = tm[t][e], y = tv[t][e];
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) {
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
@@ -503,46 +541,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
             }
           }
       }
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[t][e] += ex2(sc[t][e] - m[t][e]) + ex2(sc[t][2 + e] - m[t][e]);
-          w[e] = ex2(lv[t][e] - mv[t][e]);
-          w[2 + e] = ex2(lv[t][2 + e] - mv[t][e]);
-        }
-        pb[t][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-        pb[t][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-      }
-      // ---- O^T += V^T P^T ----------------------------------------------------
-      const uint8_t* vim = im + kv4::off_v(C) + gid * 4 * D + tig * D;
-      // (bytes of rows never written may be anything: kept finite, their weight is 0)
-      const uint32_t vs = 0x7f7f7f7fu & *reinterpret_cast<const uint32_t*>(
-          im + kv4::off_vs(C) + (C == 128 ? gid : gid >> 1) * 16 + 4 * tig);
-      const ScalePair s0 = scale_pair(vs, 0x4140, k16), s1 = scale_pair(vs, 0x4342, k16);
-      uint32_t x0[D / 4], x1[D / 4];
-      if constexpr (C == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(vim);
-        const uint4 y = *reinterpret_cast<const uint4*>(vim + 32 * D);
-        x0[0] = x.x; x0[1] = x.y; x0[2] = x.z; x0[3] = x.w;
-        x1[0] = y.x; x1[1] = y.y; x1[2] = y.z; x1[3] = y.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(vim);
-        const uint2 y = *reinterpret_cast<const uint2*>(vim + 32 * D);
-        x0[0] = x.x; x0[1] = x.y;
-        x1[0] = y.x; x1[1] = y.y;
-      }
-#pragma unroll
-      for (int w = 0; w < D / 4; ++w) {
-        uint32_t a0[4], a1[4];
-        widen4(x0[w], s0, k16, a0);
-        widen4(x1[w], s1, k16, a1);
+      for (int n = 0; n < N; ++n) {
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_16816(o[t][2 * w], a0[0], a0[1], a1[0], a1[1], pb[t][0], pb[t][1]);
-          mma_16816(o[t][2 * w + 1], a0[2], a0[3], a1[2], a1[3], pb[t][0], pb[t][1]);
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[t][e] += ex2(sc[n][t][e] - m[t][e]) + ex2(sc[n][t][2 + e] - m[t][e]);
+            w[e] = ex2(lv[n][t][e] - mv[t][e]);
+            w[2 + e] = ex2(lv[n][t][2 + e] - mv[t][e]);
+          }
+          pb[t][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+          pb[t][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+        }
+        // ---- O^T += V^T P^T --------------------------------------------------
+        const uint8_t* im = im0 + n * F::kTB;
+        const uint8_t* vim = im + kv4::off_v(C) + gid * 4 * D + tig * D;
+        // (bytes of rows never written may be anything: kept finite, their weight is 0)
+        const uint32_t vs = 0x7f7f7f7fu & *reinterpret_cast<const uint32_t*>(
+            im + kv4::off_vs(C) + (C == 128 ? gid : gid >> 1) * 16 + 4 * tig);
+        const ScalePair s0 = scale_pair(vs, 0x4140, k16), s1 = scale_pair(vs, 0x4342, k16);
+        uint32_t x0[D / 4], x1[D / 4];
+        if constexpr (C == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vim);
+          const uint4 y = *reinterpret_cast<const uint4*>(vim + 32 * D);
+          x0[0] = x.x; x0[1] = x.y; x0[2] = x.z; x0[3] = x.w;
+          x1[0] = y.x; x1[1] = y.y; x1[2] = y.z; x1[3] = y.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(vim);
+          const uint2 y = *reinterpret_cast<const uint2*>(vim + 32 * D);
+          x0[0] = x.x; x0[1] = x.y;
+          x1[0] = y.x; x1[1] = y.y;
+        }
+#pragma unroll
+        for (int w = 0; w < D / 4; ++w) {
+          uint32_t a0[4], a1[4];
+          widen4(x0[w], s0, k16, a0);
+          widen4(x1[w], s1, k16, a1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma_16816(o[t][2 * w], a0[0], a0[1], a1[0], a1[1], pb[t][0], pb[t][1]);
+            mma_16816(o[t][2 * w + 1], a0[2], a0[3], a1[2], a1[3], pb[t][0], pb[t][1]);
+          }
         }
       }
     };
@@ -550,15 +592,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
     for (; at.s < at.nu && u < units; ++at.s, ++u) {
       const int st = u % F::kStages;
       mbar_wait(&full[st], (uint32_t)((u / F::kStages) & 1), a.err);
-      const int t0 = meta[st];
-      if (t0 >= 0) image(ring + st * F::kTB, t0);
+      const int2 t0 = meta[st];
+      const uint8_t* im = ring + st * F::kStageBytes;
+      if (t0.x >= 0 && t0.y >= 0) {
+        images(std::integral_constant<int, 2>(), im, t0.x, t0.y);
+      } else if (t0.x >= 0 || t0.y >= 0) {  // the end of what is seen, or an absent block
+        images(std::integral_constant<int, 1>(), im + (t0.x >= 0 ? 0 : F::kTB), max(t0.x, t0.y), -1);
+      }
       __syncwarp();
       issue(u + F::kStages, st);
     }
     const bool ends = at.s == at.nu;
     if (ends) next_segment(at);
 
-    // ---- merge the eight warps ---------------------------------------------------
+    // ---- merge the warps ---------------------------------------------------
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -691,7 +738,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
 
 // CTAs of the decode kernel, and the head tile (n-tiles of 8) for a group.
 int dec_nt(int group) { return group <= 8 ? 1 : 2; }
-int dec_grid(int group) { return sm_count() * (dec_nt(group) == 1 ? 2 : 1); }
+int dec_grid(int group) { return sm_count() * (dec_nt(group) == 1 ? 4 : 2); }
 
 template <int C, int NT>
 cudaError_t launch_dec(const DecArgs& a, cudaStream_t s) {
