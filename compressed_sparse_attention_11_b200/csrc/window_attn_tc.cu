@@ -23,7 +23,14 @@
 // Softmax: one thread per row (two warpgroups, one per query tile), running
 // maximum that moves only past 2^8 (the row of O is then rescaled in tensor
 // memory), weights rounded to bf16 for the second product while the sum takes
-// them unrounded.
+// them unrounded.  It is the bound: a tile's 128 x 128 exponentials take the
+// special-function units 1024 cycles, the tile's two products 512 (C = 128).
+// So three of eight are formed by fmas instead (kPoly of kPolyOf pairs): x
+// split into a nearest integer and f in [-1/2, 1/2], 2^f by a degree-4
+// polynomial of least relative error (2^-18), two at a time, the integer added
+// to the exponent; the other arithmetic runs on pairs as well.  The softmax
+// warps take registers from the two others' warpgroup, so that a row of 128
+// scores stays in registers.
 //
 // A value row that is not finite where a query's mask hides it would still
 // reach that query through 0 x inf in the second product.  The epilogue sees
@@ -46,8 +53,13 @@ constexpr int kSlab = kRows * 128;  // 16 KB: 128 rows x 64 dims
 constexpr int kStages = 2;
 constexpr int kSoftWarps = 8;  // two warpgroups
 constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + 1;
-constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kThreads = (kSoftWarps + 4) * 32;  // two idle warps fill the last warpgroup
+// Registers a thread: 168 x 384 at launch, moved between the warpgroups:
+// 208 x 256 + 88 x 128 = 168 x 384.
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
+static_assert(kSoftRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "register split");
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kPoly = 0, kPolyOf = 8;  // of so many pairs of exponentials, so many by polynomial
 
 struct WinArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -113,15 +125,48 @@ __device__ __forceinline__ int first_cols(const WinArgs& a, const Job& j, int tj
 __device__ __forceinline__ bool active(const WinArgs& a, const Job& j, int q) {
   return j.i0 + q * a.tt < a.nq;
 }
-// Whether a row of query tile q sees a key of tile tj.
-__device__ __forceinline__ bool needs(const WinArgs& a, const Job& j, int q, int tj) {
-  if (!active(a, j, q)) return false;
-  const int ta = j.t0 + q * a.tt, tb = min(ta + a.tt - 1, j.t1), base = j.base(tj);
-  if (base > tb) return false;
-  return (ta - a.window + 1 - base < kKeys && (tj + 1) * kKeys > j.f8) || first_cols(a, j, tj) > 0;
+// The key tiles that some row of query tile q sees: those below nf (first
+// tokens) and w0 .. w1 (window).
+struct Need {
+  int nf, w0, w1;
+  __device__ int begin() const { return nf > 0 ? 0 : w0; }
+  __device__ bool has(int t) const { return (t < nf || t >= w0) && t <= w1; }
+  __device__ int next(int t) const { return t + 1 >= nf && t + 1 < w0 ? w0 : t + 1; }
+};
+__device__ __forceinline__ Need need_of(const WinArgs& a, const Job& j, int q) {
+  Need n;
+  if (!active(a, j, q)) {
+    n.nf = n.w0 = 0;
+    n.w1 = -1;
+    return n;
+  }
+  const int ta = j.t0 + q * a.tt, tb = min(ta + a.tt - 1, j.t1), v0 = j.klo - j.f8;
+  n.w0 = max(0, ta - a.window + 1 - v0) / kKeys;
+  n.w1 = (tb - v0) / kKeys;
+  n.nf = j.f8 > 0 || j.klo == 0 ? min((a.first + kKeys - 1) / kKeys, n.w1 + 1) : 0;
+  return n;
 }
 
-// (q, k) of a row and key in fp32, the lanes of the warp sharing the dims.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 2^x of two values, relative error 2^-18; x <= 100 (below -126: 2^-126).
+__device__ __forceinline__ float2 poly_ex2(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 n = add2(x, make_float2(12582912.f, 12582912.f));  // 1.5 2^23: the integer in the low bits
+  const float2 f = add2(x, add2(make_float2(12582912.f, 12582912.f), make_float2(-n.x, -n.y)));
+  float2 p = fma2(f, make_float2(0.009570101276f, 0.009570101276f), make_float2(0.055917862803f, 0.055917862803f));
+  p = fma2(p, f, make_float2(0.240247443318f, 0.240247443318f));
+  p = fma2(p, f, make_float2(0.693121790886f, 0.693121790886f));
+  p = fma2(p, f, make_float2(0.999999284744f, 0.999999284744f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(n.y) << 23)));
+}
+
+// One row again in fp32, the lanes of the warp sharing the dims.
 template <int C>
 __device__ __noinline__ void exact_row(const WinArgs& a, const Job& j, int i, int head, float m,
                                        float inv, __nv_bfloat16* out) {
@@ -200,6 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
 
+  if (warp >= kSoftWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kTmaWarp) {
     // ================================ TMA producer ================================
     int n = 0;               // key tiles issued
@@ -272,100 +319,88 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     // ================================ MMA issuer ==================================
     constexpr uint32_t kIdQK = idesc_bf16(kRows, kKeys, 0, 0);
     constexpr uint32_t kIdPV = idesc_bf16(kRows, C, 0, 1);
-    const uint32_t q0 = smem_u32(smem + F::off_q), k0 = smem_u32(smem + F::off_k),
-                   v0 = smem_u32(smem + F::off_v);
-    int n = 0;                    // key tiles of all jobs
-    int v_next = 0;               // next value tile to be freed
-    int pend[2] = {-1, -1};       // key tile whose P.V is still to be issued
-    bool pend_first[2], pend_last[2];
-    int pvs[2] = {0, 0}, jobs[2] = {0, 0}, done[2] = {0, 0};  // P.V issued, query tiles begun / finished
+    // descriptors of stage / query tile 0; offsets in 16-byte units
+    const uint32_t leader = lane == 0 ? 1u : 0u, tm = uniform(tmem);
+    const uint32_t sm = uniform(smem_u32(smem));
+    const DescWords dq(desc_sw128(sm + F::off_q)), dk(desc_sw128(sm + F::off_k)),
+        dv(desc_sw128_mn(sm + F::off_v, kSlab, 1024));
+    constexpr uint32_t kTile16 = F::kTileBytes / 16, kSlab16 = kSlab / 16;
+    int n = 0;                             // key tiles of all jobs
+    int pvs[2] = {0, 0}, jobs[2] = {0, 0};  // P.V issued, query tiles finished
     bool ok = true;
-    auto issue_pv = [&](int q) -> bool {
-      const int st = pend[q] % kStages;
-      if (!mbar_wait(&bar->p_full[q], (uint32_t)(pvs[q] & 1), err)) return false;
-      if (!mbar_wait(&bar->v_full[st], (uint32_t)((pend[q] / kStages) & 1), err)) return false;
+    // weights of key tile k (its values in stage k % kStages) into O_q
+    auto issue_pv = [&](int q, int k, bool first, bool last) -> bool {
+      const int st = k % kStages;
+      if (!mbar_wait(&bar->v_full[st], (uint32_t)((k / kStages) & 1), err)) return false;
       // the first P.V of a query tile overwrites O: the epilogue before has read it
-      if (pend_first[q] && done[q] > 0 &&
-          !mbar_wait(&bar->o_free[q], (uint32_t)((done[q] - 1) & 1), err))
+      if (first && jobs[q] > 0 && !mbar_wait(&bar->o_free[q], (uint32_t)((jobs[q] - 1) & 1), err))
         return false;
-      tc_fence_after();
-      if (lane == 0) {
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_bf16_ts(tmem + F::col_o + q * C, tmem + F::col_s + q * kKeys + kk * 8,
-                      desc_sw128_mn(v0 + st * F::kTileBytes + kk * 2048, kSlab, 1024), kIdPV,
-                      (pend_first[q] && kk == 0) ? 0u : 1u);
-        if (pend_last[q]) mma_commit(&bar->o_full[q]);
-      }
-      __syncwarp();
-      if (pend_last[q]) ++done[q];
+      if (!mbar_wait(&bar->p_full[q], (uint32_t)(pvs[q] & 1), err)) return false;
       ++pvs[q];
-      pend[q] = -1;
-      return true;
-    };
-    // value tiles that no P.V to come reads
-    auto free_v = [&](int upto) {
-      while (v_next < upto && v_next != pend[0] && v_next != pend[1]) {
-        if (lane == 0) mma_commit(&bar->v_free[v_next % kStages]);
-        ++v_next;
+      tc_fence_after();
+      const uint32_t d = tm + F::col_o + q * C, p = tm + F::col_s + q * kKeys;
+      const uint32_t v = dv.lo + uniform(st * kTile16), acc = uniform(first ? 0u : 1u);
+#pragma unroll
+      for (int kk = 0; kk < kKeys / 16; ++kk)
+        mma_bf16_ts_w(leader, d, p + kk * 8, v + kk * 128, dv.hi, kIdPV, kk == 0 ? acc : 1u);
+      if (last) {
+        if (lane == 0) mma_commit(&bar->o_full[q]);
+        ++jobs[q];
       }
-      __syncwarp();
+      return true;
     };
     for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
       const Job jb = job_of(a, w);
-      bool first[2] = {true, true};
-      int last[2];
-      for (int q = 0; q < 2; ++q) {
-        last[q] = jb.tiles - 1;
-        while (last[q] >= 0 && !needs(a, jb, q, last[q])) --last[q];
-      }
-      for (int tj = 0; tj < jb.tiles && ok; ++tj, ++n) {
+      const Need need[2] = {need_of(a, jb, 0), need_of(a, jb, 1)};
+      bool pend[2] = {false, false}, begun[2] = {false, false};
+      for (int tj = 0; tj <= jb.tiles && ok; ++tj) {
         const int st = n % kStages;
         bool have_k = false;
-        for (int q = 0; q < 2 && ok; ++q) {
-          // the value ring never waits for a query tile that has no more work
-          if (pend[q] >= 0) {
-            if (!(ok = issue_pv(q))) break;
-            free_v(n);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (ok && pend[q]) {  // the tile before this one
+            ok = issue_pv(q, n - 1, !begun[q], tj - 1 == need[q].w1);
+            begun[q] = true;
           }
-          if (!needs(a, jb, q, tj)) continue;
-          if (first[q] && !(ok = mbar_wait(&bar->q_full[q], (uint32_t)(jobs[q] & 1), err))) break;
-          if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err))) break;
+          pend[q] = tj < jb.tiles && need[q].has(tj);
+          if (!ok || !pend[q]) continue;
+          if (tj == need[q].begin() && !(ok = mbar_wait(&bar->q_full[q], (uint32_t)(jobs[q] & 1), err))) continue;
+          if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err))) continue;
           have_k = true;
           tc_fence_after();
-          if (lane == 0) {
+          // (in order behind the P.V that reads the weights out of these columns)
+          const uint32_t d = tm + F::col_s + q * kKeys;
+          const uint32_t k0 = dk.lo + uniform(st * kTile16), qq = dq.lo + q * kTile16;
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk)
-              mma_bf16(tmem + F::col_s + q * kKeys,
-                       desc_sw128(q0 + q * F::kTileBytes + (kk >> 2) * kSlab + (kk & 3) * 32),
-                       desc_sw128(k0 + st * F::kTileBytes + (kk >> 2) * kSlab + (kk & 3) * 32),
-                       kIdQK, kk != 0 ? 1u : 0u);
+          for (int kk = 0; kk < C / 16; ++kk) {
+            const uint32_t step = (kk >> 2) * kSlab16 + (kk & 3) * 2;
+            mma_bf16_w(leader, d, qq + step, dq.hi, k0 + step, dk.hi, kIdQK, kk != 0 ? 1u : 0u);
+          }
+          if (lane == 0) {
             mma_commit(&bar->s_full[q]);
-            if (tj == last[q]) mma_commit(&bar->q_free[q]);
+            if (tj == need[q].w1) mma_commit(&bar->q_free[q]);
           }
           __syncwarp();
-          pend[q] = n;
-          pend_first[q] = first[q];
-          pend_last[q] = tj == last[q];
-          if (first[q]) ++jobs[q];
-          first[q] = false;
         }
         if (!ok) break;
-        // a tile that no row needs was loaded all the same: wait for it, then free it
-        if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err) &&
-                              mbar_wait(&bar->v_full[st], (uint32_t)((n / kStages) & 1), err)))
-          break;
-        if (lane == 0) mma_commit(&bar->k_free[st]);
+        if (tj > 0 && lane == 0) mma_commit(&bar->v_free[(n - 1) % kStages]);
+        if (tj < jb.tiles) {
+          // (a tile that no row needs was loaded all the same)
+          if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err) &&
+                                mbar_wait(&bar->v_full[st], (uint32_t)((n / kStages) & 1), err)))
+            break;
+          if (lane == 0) mma_commit(&bar->k_free[st]);
+          ++n;
+        }
         __syncwarp();
-        free_v(n);
       }
     }
-    for (int q = 0; q < 2 && ok; ++q)
-      if (pend[q] >= 0) ok = issue_pv(q);
     if (lane == 0) mma_commit(&bar->drain);
     __syncwarp();
     mbar_wait(&bar->drain, 0, err, false);
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ============================ softmax and epilogue ============================
     const int q = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
@@ -378,14 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     bool ok = true;
     for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
       const Job jb = job_of(a, w);
-      if (!active(a, jb, q)) continue;
+      const Need need = need_of(a, jb, q);
+      if (need.w1 < 0) continue;
       const int ta = jb.t0 + q * a.tt, t = ta + tl;
       const int tb = min(ta + a.tt - 1, jb.t1);
       float m = kNegInf, l = 0.f;
-      int t_first = -1;  // the first tile that the query tile needs (O is not yet written there)
-      for (int tj = 0; tj < jb.tiles; ++tj) {
-        if (!needs(a, jb, q, tj)) continue;
-        if (t_first < 0) t_first = tj;
+      const int t_first = need.begin();  // (O is not yet written there)
+      for (int tj = t_first; tj <= need.w1; tj = need.next(tj)) {
         if (!(ok = mbar_wait(&bar->s_full[q], (uint32_t)(steps & 1), err))) break;
         ++steps;
         tc_fence_after();
@@ -398,17 +432,26 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
 #pragma unroll
           for (int i = 0; i < kKeys; ++i) s[i] = -s[i];
         }
-        const int base = jb.base(tj), fc = first_cols(a, jb, tj);
-        if (base + kKeys - 1 > ta || tb - a.window + 1 > base) {  // some row hides a key
-          const int hi = t - base, lo = t - a.window + 1 - base;
+        const int base = jb.base(tj);
+        if (base + kKeys - 1 > ta) {  // keys behind a row's own token
+          const int hi = t - base;
 #pragma unroll
           for (int i = 0; i < kKeys; ++i)
-            if (!(i <= hi && (i >= lo || i < fc))) s[i] = kNegInf;
+            if (i > hi) s[i] = kNegInf;
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        if (tb - a.window + 1 > base) {  // keys before a row's window that are no first tokens
+          const int lo = t - a.window + 1 - base, fc = first_cols(a, jb, tj);
 #pragma unroll
-        for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.qs;
+          for (int i = 0; i < kKeys; ++i)
+            if (i < lo && i >= fc) s[i] = kNegInf;
+        }
+        float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]),
+                       max3(s[9], s[10], s[11])};
+#pragma unroll
+        for (int i = 12; i < kKeys - 4; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
+        mx[0] = max3(mx[0], s[kKeys - 4], s[kKeys - 3]);
+        mx[1] = max3(mx[1], s[kKeys - 2], s[kKeys - 1]);
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.qs;
         const bool grow = top > m + kRescaleLog2;
         if (__any_sync(0xffffffffu, grow)) {
           // O is complete up to the tile before: its P.V was issued before this S
@@ -430,21 +473,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
           m = mn;
         }
         const float mr = m == kNegInf ? 0.f : m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 qs2 = make_float2(a.qs, a.qs), mr2 = make_float2(-mr, -mr);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            const float p0 = ex2(fmaf(s[64 * c + i], a.qs, -mr));
-            const float p1 = ex2(fmaf(s[64 * c + i + 1], a.qs, -mr));
-            ls[i & 3] += p0;
-            ls[(i & 3) + 1] += p1;
-            pk[i >> 1] = pack_bf16x2(p0, p1);
+          for (int i = 0; i < 32; ++i) {
+            const float2 x = fma2(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), qs2, mr2);
+            const float2 p = (i * kPoly) % kPolyOf < kPoly ? poly_ex2(x) : make_float2(ex2(x.x), ex2(x.y));
+            ls[i & 1] = add2(ls[i & 1], p);
+            pk[i] = pack_bf16x2(p.x, p.y);
           }
           tmem_st32(s_addr + c * 32, pk);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
