@@ -23,14 +23,19 @@
 // Softmax: one thread per row (two warpgroups, one per query tile), running
 // maximum that moves only past 2^8 (the row of O is then rescaled in tensor
 // memory), weights rounded to bf16 for the second product while the sum takes
-// them unrounded.  It is the bound: a tile's 128 x 128 exponentials take the
-// special-function units 1024 cycles, the tile's two products 512 (C = 128).
-// So three of eight are formed by fmas instead (kPoly of kPolyOf pairs): x
-// split into a nearest integer and f in [-1/2, 1/2], 2^f by a degree-4
-// polynomial of least relative error (2^-18), two at a time, the integer added
-// to the exponent; the other arithmetic runs on pairs as well.  The softmax
-// warps take registers from the two others' warpgroup, so that a row of 128
-// scores stays in registers.
+// them unrounded; the arithmetic runs on pairs (fma.f32x2).  The softmax warps
+// take registers from the two others' warpgroup, so that a row of 128 scores
+// stays in registers.
+//
+// What bounds it: a query tile's products of one key tile need the tensor cores
+// for 1024 cycles and its 128 x 128 exponentials the special-function units
+// for as many, so two query tiles could share 2048 cycles.  Its chain, though,
+// is S -> softmax (2200 cycles: 300 to read S, 300 for the maximum, 1450 for
+// exponentials that meet the other warpgroup's, 150 to store P) -> P.V -> next
+// S (1700 with the wait for the other tile's products): 3900, as P lives in S's
+// columns and the next S cannot start before P.V has read them (tensor memory
+// is full).  2 x 8192 tokens, 32 heads over 8, W = 1024, 4 first tokens,
+// C = 128: 308 us, 840 TFLOP/s.
 //
 // A value row that is not finite where a query's mask hides it would still
 // reach that query through 0 x inf in the second product.  The epilogue sees
@@ -59,7 +64,6 @@ constexpr int kThreads = (kSoftWarps + 4) * 32;  // two idle warps fill the last
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 static_assert(kSoftRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "register split");
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kPoly = 0, kPolyOf = 8;  // of so many pairs of exponentials, so many by polynomial
 
 struct WinArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -67,7 +71,7 @@ struct WinArgs {
   const float* sink;
   __nv_bfloat16* out;
   unsigned int* err;
-  int64_t works;
+  int works;
   int nq, nk, window, first, nh, nkv, group, tt, pairs;
   float qs;  // |scale| log2(e), never 0
   int neg;   // the scale is negative
@@ -103,12 +107,12 @@ struct Job {
   int klo, f8, tiles;  // see the head comment
   __device__ int base(int j) const { return klo - f8 + j * kKeys; }  // token of column 0 (window part)
 };
-__device__ __forceinline__ Job job_of(const WinArgs& a, int64_t w) {
+__device__ __forceinline__ Job job_of(const WinArgs& a, int w) {
   Job j;
-  const int pair = (int)(w % a.pairs);
-  const int64_t r = w / a.pairs;
-  j.h = (int)(r % a.nkv);
-  j.b = (int)(r / a.nkv);
+  const unsigned r = (unsigned)w / (unsigned)a.pairs;
+  const int pair = w - (int)r * a.pairs;
+  j.b = (int)(r / (unsigned)a.nkv);
+  j.h = (int)r - j.b * a.nkv;
   j.i0 = pair * 2 * a.tt;
   j.t0 = a.nk - a.nq + j.i0;
   j.t1 = a.nk - a.nq + min(a.nq, j.i0 + 2 * a.tt) - 1;
@@ -152,20 +156,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 2^x of two values, relative error 2^-18; x <= 100 (below -126: 2^-126).
-__device__ __forceinline__ float2 poly_ex2(float2 x) {
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  const float2 n = add2(x, make_float2(12582912.f, 12582912.f));  // 1.5 2^23: the integer in the low bits
-  const float2 f = add2(x, add2(make_float2(12582912.f, 12582912.f), make_float2(-n.x, -n.y)));
-  float2 p = fma2(f, make_float2(0.009570101276f, 0.009570101276f), make_float2(0.055917862803f, 0.055917862803f));
-  p = fma2(p, f, make_float2(0.240247443318f, 0.240247443318f));
-  p = fma2(p, f, make_float2(0.693121790886f, 0.693121790886f));
-  p = fma2(p, f, make_float2(0.999999284744f, 0.999999284744f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(n.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(n.y) << 23)));
-}
-
 // One row again in fp32, the lanes of the warp sharing the dims.
 template <int C>
 __device__ __noinline__ void exact_row(const WinArgs& a, const Job& j, int i, int head, float m,
@@ -252,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     int n = 0;               // key tiles issued
     int nq[2] = {0, 0};      // query tiles issued
     bool ok = true;
-    for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+    for (int w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
       const Job jb = job_of(a, w);
       auto load_q = [&](int q) {
         if (!active(a, jb, q)) return;
@@ -349,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
       }
       return true;
     };
-    for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+    for (int w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
       const Job jb = job_of(a, w);
       const Need need[2] = {need_of(a, jb, 0), need_of(a, jb, 1)};
       bool pend[2] = {false, false}, begun[2] = {false, false};
@@ -411,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     int steps = 0, jobs = 0;
     uint32_t wg_phase = 0;
     bool ok = true;
-    for (int64_t w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+    for (int w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
       const Job jb = job_of(a, w);
       const Need need = need_of(a, jb, q);
       if (need.w1 < 0) continue;
@@ -481,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float2 x = fma2(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), qs2, mr2);
-            const float2 p = (i * kPoly) % kPolyOf < kPoly ? poly_ex2(x) : make_float2(ex2(x.x), ex2(x.y));
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
             ls[i & 1] = add2(ls[i & 1], p);
             pk[i] = pack_bf16x2(p.x, p.y);
           }
@@ -619,7 +609,7 @@ cudaError_t launch_window_attn_tc(const void* q, int64_t q_stride, const void* k
   a.group = nh / nkv;
   a.tt = kRows / a.group;
   a.pairs = (int)((n_q + 2 * a.tt - 1) / (2 * a.tt));
-  a.works = (int64_t)a.pairs * nkv * batch;
+  a.works = (int)((int64_t)a.pairs * nkv * batch);
   a.neg = scale < 0.f;
   // a scale of 0 weighs every visible key alike, as does this
   a.qs = std::max(std::abs(scale) * kLog2e, 1e-30f);
