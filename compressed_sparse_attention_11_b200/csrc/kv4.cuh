@@ -62,29 +62,61 @@ struct Quant8 {
   uint32_t E;
 };
 
-// Largest |x| of 8 values as bits (infinities and NaN order above all others).
-__device__ __forceinline__ uint32_t top_bits(const uint4& w) {  // bf16 pairs
+// Largest |x| of 8 bf16 values as bits (infinities and NaN order above all others).
+__device__ __forceinline__ uint32_t top_bits(const uint4& w) {
   const uint32_t m = 0x7fff7fffu;
   const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
   return max(a & 0xffff0000u, a << 16);
 }
-__device__ __forceinline__ uint32_t top_bits(const float v[8]) {
-  uint32_t a = 0;
+
+// Eight consecutive values of a row as loaded; top(): the largest |x| as bits.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  static constexpr bool kFewBits = true;
+  uint4 w;
+  __device__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ uint32_t top() const { return top_bits(w); }
+  __device__ float2 pair(int i) const {
+    const uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  }
+};
+template <>
+struct Raw8<float> {
+  static constexpr bool kFewBits = false;
+  float w[8];
+  __device__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
-  return a;
-}
+    for (int i = 0; i < 8; ++i) w[i] = 0.f;
+  }
+  __device__ void load(const float* p) { load8(p, w); }
+  __device__ uint32_t top() const {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(w[i]) & 0x7fffffffu);
+    return a;
+  }
+  __device__ float2 pair(int i) const { return make_float2(w[2 * i], w[2 * i + 1]); }
+};
 
 // Quantises 8 values of a row spread over `lanes` neighbouring lanes (8
-// values each, lane pairs (2 i, 2 i + 1) forming a group of 16); a = their
-// top_bits.  Every lane of the warp calls it.
+// values each, lane pairs (2 i, 2 i + 1) forming a group of 16).  Every lane of
+// the warp calls it.
 //
-// The quotient x / (s r) without a division per value: x times the correctly
-// rounded reciprocal, corrected once by the exact remainder, is the correctly
-// rounded quotient, so a tie between two codes stays one, and adding 1.5 2^23
-// rounds it to nearest even.  A code can lie beyond 7 only for a subnormal s;
-// such groups, and rows near the ends of fp32's range, divide and clamp.
-__device__ __forceinline__ Quant8 quantise8(const float v[8], uint32_t a, int lanes) {
+// No division per value.  bf16: the quotient is a tie k + 1/2 exactly or at
+// least 2^-10 away from one, and x times an approximate reciprocal is within
+// 7.5 2^-23 of it; adding 6144 rounds that sum to a multiple of 2^-11, which
+// restores a tie and moves nothing across one; adding the rest of 1.5 2^23 + 8
+// then rounds to nearest even.  fp32: x times the correctly rounded
+// reciprocal, corrected once by the exact remainder, is the correctly rounded
+// quotient.  A code can lie beyond 7 only for a subnormal s; such groups, and
+// rows near the ends of fp32's range, divide and clamp.
+template <typename T>
+__device__ __forceinline__ Quant8 quantise8(const Raw8<T>& raw, int lanes) {
+  uint32_t a = raw.top();
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
   uint32_t top = a;
   for (int off = lanes >> 1; off > 1; off >>= 1)
@@ -95,19 +127,35 @@ __device__ __forceinline__ Quant8 quantise8(const float v[8], uint32_t a, int la
   q.scale = 0;
   q.E = 255;
   if (ex == 255) return q;
-  q.E = (uint32_t)min(max(ex - 10, 1), 254);
-  const float r = __uint_as_float(q.E << 23);
-  q.scale = e4m3_code(__fdiv_rn(__uint_as_float(a), 7.f * r));
-  const float step = e4m3_value((uint8_t)q.scale) * r;
+  q.E = (uint32_t)max(ex - 10, 1);
+  // a / (7 r), correctly rounded: a / r is exact, the remainder of the first
+  // quotient by 7 too
+  const float ar = __uint_as_float(a) * __uint_as_float((254u - q.E) << 23);
+  const float q0 = ar * (1.f / 7.f);
+  q.scale = e4m3_code(fmaf(fmaf(-q0, 7.f, ar), 1.f / 7.f, q0));
+  const float step = e4m3_value((uint8_t)q.scale) * __uint_as_float(q.E << 23);
   if (step == 0.f) return q;
   if (q.scale >= 8 && q.E > 24 && q.E < 230) {
-    const float inv = __frcp_rn(step);
     uint32_t acc = 0;
+    if (Raw8<T>::kFewBits) {
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      const float t = v[i] * inv;
-      const float x = fmaf(fmaf(-t, step, v[i]), inv, t);
-      acc = acc * 16u + __float_as_uint(x + 12582920.f);  // 0x4b400000 + code + 8
+      for (int i = 3; i >= 0; --i) {
+        const float2 x = add2(fma2(raw.pair(i), inv2, make_float2(6144.f, 6144.f)),
+                              make_float2(12576776.f, 12576776.f));  // 0x4b400000 + code + 8
+        acc = acc * 16u + __float_as_uint(x.y);
+        acc = acc * 16u + __float_as_uint(x.x);
+      }
+    } else {
+      const float inv = __frcp_rn(step);
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        const float2 v2 = raw.pair(i >> 1);
+        const float v = i & 1 ? v2.y : v2.x, t = v * inv;
+        acc = acc * 16u + __float_as_uint(fmaf(fmaf(-t, step, v), inv, t) + 12582920.f);
+      }
     }
     q.codes = acc - 0x3f400000u;  // 0x4b400000 (1 + 16 + 16^2 + ...) mod 2^32
     return q;
@@ -115,11 +163,71 @@ __device__ __forceinline__ Quant8 quantise8(const float v[8], uint32_t a, int la
   q.codes = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = rintf(__fdiv_rn(v[i], step));
+    const float2 v2 = raw.pair(i >> 1);
+    const float x = rintf(__fdiv_rn(i & 1 ? v2.y : v2.x, step));
     q.codes |= (uint32_t)((int)fminf(fmaxf(x, -7.f), 7.f) + 8) << (4 * i);
   }
   return q;
 }
+
+// The eight values r s code of codes w (nibble j: value j).
+__device__ __forceinline__ void store_values(float* p, uint32_t w, uint32_t s, uint32_t E) {
+  const float step = e4m3_value((uint8_t)s), r = row_scale(E);
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)  // 2^23 + nibble
+    x[j] = (__uint_as_float(0x4b000000u | ((w >> (4 * j)) & 15u)) - 8388616.f) * step * r;
+  store8(p, x);
+}
+// bf16: pairs (j, j + 4) of 128 + nibble, times r s, less 136 r s: one fma, each
+// part of it exact (s has 4 significant bits, 136 s = 17 s 8 has 8).
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint32_t s, uint32_t E) {
+  if (E - 24u > 206u) {  // near the ends of the range, or 255
+    const float step = e4m3_value((uint8_t)s), r = row_scale(E);
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (float)((int)((w >> (4 * j)) & 15u) - 8) * step * r;
+    store8(p, x);
+    return;
+  }
+  const float sr = e4m3_value((uint8_t)s) * __uint_as_float(E << 23);
+  const __nv_bfloat162 m = __float2bfloat162_rn(sr), c = __float2bfloat162_rn(-136.f * sr);
+  uint32_t h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 x = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&n), m, c);
+    h[j] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410),
+                 __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
+}
+
+// Where a lane's part of a row lies in an image: eight dims from 8 sub of a
+// key (is_v = 0) or value row.  For token u = 4 t + 2 h + b every offset is
+// base + h X + t Y + b Z: the codes' two halves lie `half` bytes apart.
+template <int C>
+struct LanePart {
+  int codes, half, code_t, code_b, scale, scale_h, scale_t, scale_b, exp;
+  __device__ __forceinline__ LanePart(bool is_v, int sub)
+      : codes(is_v ? off_v(C) + v_pair(C, 0, sub * 8) : sub * 4),
+        half(is_v ? 4 : 2),
+        code_t(is_v ? C / 8 : C),
+        code_b(is_v ? 2 : C / 2),
+        scale(is_v ? off_vs(C) + (sub >> 1) * 16 : off_ks(C) + (sub >> 1)),
+        scale_h(is_v ? 2 : C / 2),
+        scale_t(is_v ? 4 : C / 8),
+        scale_b(is_v ? 1 : C / 16),
+        exp(off_exp(C) + (is_v ? 1 : 0)) {}
+  __device__ __forceinline__ int code_at(int u) const {
+    return codes + ((u >> 1) & 1) * 4 * C + (u >> 2) * code_t + (u & 1) * code_b;
+  }
+  __device__ __forceinline__ int scale_at(int u) const {
+    return scale + ((u >> 1) & 1) * scale_h + (u >> 2) * scale_t + (u & 1) * scale_b;
+  }
+  __device__ __forceinline__ int exp_at(int u) const { return exp + 2 * slot_of(u); }
+};
 
 }  // namespace kv4
 }  // namespace csa
