@@ -594,9 +594,11 @@ def _kv4_desc(cache: torch.Tensor, block_table: torch.Tensor):
     if cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("cache must be a uint8 [num_blocks, nkv, block_tokens / 16, bytes] tensor "
                          "and block_table an int32 [batch, max_blocks] tensor")
-    dev = _device(cache)
     nb, nkv, tiles, by = cache.shape
     c = (by - 32) // 18
+    if by != 18 * c + 32:
+        raise ValueError("the last dim of cache must be 18 c + 32 bytes")
+    dev = _device(cache)
     return dev, Kv4Desc(_dense(cache, dev, torch.uint8, "cache"),
                         _dense(block_table, dev, torch.int32, "block_table"), *block_table.shape,
                         nb, nkv, c, 16 * tiles), nkv, c

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const T* __restr
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y;
   const int64_t p0 = a.pos[b];
-  if (p0 < 0) return;
+  if (p0 < 0 || p0 > (int64_t)1 << 62) return;  // (the latter: behind every table)
   int64_t n = a.n;
   if (a.count != nullptr) n = min(n, (int64_t)max(0, a.count[b]));
   const int64_t tile = p0 / 16 + (int64_t)blockIdx.x * kWarps + warp;
@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fetch_kernel(const Kv4Rows a,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y;
-  const int64_t p0 = a.pos[b];
+  int64_t p0 = a.pos[b];
+  if (p0 > (int64_t)1 << 62) p0 = -1;  // behind every table
   int64_t n = a.n;  // rows that are there; the others come back as zeros
   if (a.count != nullptr) n = min(n, (int64_t)max(0, a.count[b]));
   if (p0 < 0) n = 0;

@@ -46,7 +46,7 @@ extern "C" csa_status csa_window_attn(const void* q, int64_t q_stride, const voi
                                 n_q, nh, c, 1, dt, nullptr, out, s, first),
                     "csa_window_attn");
   }
-  API_SUPPORTED(batch * n_q * nkv < ((int64_t)1 << 31), "csa_window_attn: too many rows");
+  API_SUPPORTED(batch <= (((int64_t)1 << 31) - 1) / nkv / n_q, "csa_window_attn: too many rows");
   unsigned int* flag = device_timeout_flag();
   if (flag == nullptr) return set_last_error(CSA_ERR_CUDA, "csa_window_attn: no device flag");
   return api_cuda(launch_window_attn_tc(q, q_stride, k, k_stride, v, v_stride, window, first, sink,

@@ -484,7 +484,8 @@ csa_status csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
  *       and n_k times those
  *   v NULL: shared rows, each key row is its own value (nkv = 1, n_q = n_k,
  *       dense) -- the window-only layers of the CSA / HCA stack
- * Needs: separate values: bf16, c = 64 or 128; shared rows: c % 32 == 0 and
+ * Needs: separate values: bf16, c = 64 or 128, nh / nkv <= 128 and fewer than
+ * 2^31 rows batch * n_q * nkv; shared rows: c % 32 == 0 and
  * c <= 512, fp32 or bf16 (64 heads x 512 on the tensor cores).  Else
  * CSA_ERR_UNSUPPORTED.  out must not overlap an input.
  * ------------------------------------------------------------------------ */
@@ -505,6 +506,7 @@ csa_status csa_window_attn(const void* q, int64_t q_stride, const void* k, int64
  *   s (E4M3) for each 16 values: max|x| of them / (7 r)
  *   code (4 bits): x / (s r) rounded to nearest even, in -7 .. 7 (0 if s = 0),
  *     stored as code + 8;            the row's values are r s code.
+ *     A row with E = 255 has s = 0 and codes 0 (stored 8) throughout.
  * All steps in fp32.  A block holds [nkv][block_tokens / 16] images of 16
  * tokens, 18 c + 32 bytes each:
  *   K codes [slot][c/2], V codes [h][8][t][c/32][b][2], K scales [slot][c/16],

@@ -111,6 +111,20 @@ def test_absent_blocks_are_not_written_and_read_as_zeros():
     assert torch.equal((y[0, :, 0, 0] != 0).cpu(), there)
 
 
+def test_positions_behind_every_table():
+    cache = csa.csa_kv4_cache(4, 1, 64, 16)
+    table = torch.arange(4, dtype=torch.int32, device=DEV).reshape(2, 2)
+    k = torch.ones((2, 5, 1, 64), dtype=torch.bfloat16, device=DEV)
+    for p in (32, 2 ** 31, 2 ** 40, 2 ** 63 - 3):
+        pos = torch.tensor([p, 3], dtype=torch.int64, device=DEV)
+        csa.csa_kv4_store(cache, table, pos, k, k)
+        assert torch.count_nonzero(cache[:2]) == 0
+        for y in csa.csa_kv4_fetch(cache, table, pos, 5):
+            # a row of ones: r = 2^-10, s = E4M3(1024 / 7 = 146.3) = 144 (steps of 16),
+            # code = rint(1024 / 144 = 7.1) = 7: 7 * 144 / 1024
+            assert torch.count_nonzero(y[0]) == 0 and (y[1] == 63 / 64).all()
+
+
 # ------------------------------------------------------------------- attention ---
 
 def decode_case(c, nkv, g, P, lens, W, first, sink, seed, scale=None):

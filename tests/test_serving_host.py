@@ -108,6 +108,8 @@ def window(**kw):
     (dict(c=96, qs=768), UNSUP, "c = 64 or 128"),
     (dict(nh=258, nkv=2, qs=258 * 128), UNSUP, "nh / nkv"),
     (dict(nk=1 << 31), UNSUP, "2^30"),
+    (dict(B=1 << 20, nq=1 << 12, nk=1 << 12), UNSUP, "too many rows"),
+    (dict(B=(1 << 31) - 1, nq=1 << 29, nk=1 << 29), UNSUP, "too many rows"),     # the product passes 2^60
     (dict(v=None), UNSUP, "shared"),
     (dict(v=None, nkv=1, nq=4, ks=128), UNSUP, "shared"),
     (dict(v=None, nkv=1, ks=256), UNSUP, "shared"),
@@ -281,5 +283,7 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
                  lambda: csa.csa_blocks_free(tab.long(), i32, 4), lambda: csa.csa_blocks_fork(tab[0], i32, i32, i64, i32)):
         with pytest.raises(ValueError):
             call()
+    with pytest.raises(ValueError, match="18 c"):      # the rows of no head dim
+        csa.csa_kv4_fetch(torch.zeros((4, 2, 2, 18 * 128 + 48), dtype=torch.uint8), tab, i64, 4)
     csa.csa_blocks_copy([], i32, i32)      # no regions: nothing to do
 
