@@ -457,6 +457,11 @@ def _dense(t: Optional[torch.Tensor], dev: int, dtype, name: str, numel: int = -
     return t.data_ptr()
 
 
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of x's shape and type (a third of torch.empty's host time)."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _tokens_view(x: torch.Tensor, name: str):
     """(tokens, stride) of x [..., heads, c] whose heads are dense and whose
     leading dims step by one token stride (elements)."""
@@ -500,7 +505,7 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
         nh = q.shape[-2]
         tokens, qs = _tokens_view(q, "q")
         if q_out is None:
-            q_out, qos = torch.empty(q.shape, dtype=dtype, device=q.device), nh * c
+            q_out, qos = _like(q), nh * c
         else:
             if q_out.shape != q.shape or q_out.dtype != dtype or q_out.get_device() != dev:
                 raise ValueError("q_out must be like q")
@@ -517,7 +522,7 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
             raise ValueError("q and k must have the same tokens, head dim, dtype and device")
         tokens = n
         if k_out is None:
-            k_out, kos = torch.empty(k.shape, dtype=dtype, device=k.device), nkv * c
+            k_out, kos = _like(k), nkv * c
         else:
             if k_out.shape != k.shape or k_out.dtype != dtype or k_out.get_device() != dev:
                 raise ValueError("k_out must be like k")
@@ -564,7 +569,7 @@ def csa_window_attn(q, k, v, window: int, first: int = 0, sink=None, scale: floa
             raise ValueError("v must be like k")
         vp, vs = v.data_ptr(), _tokens_view(v, "v")[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        out = _like(q)
     elif out.shape != q.shape:
         raise ValueError("out must be like q")
     _call(lib().csa_window_attn, dev, q.data_ptr(), _tokens_view(q, "q")[1], k.data_ptr(),
@@ -647,7 +652,7 @@ def csa_kv4_decode_attn(q, cache, block_table, pos, scale: float, window: int = 
     B, nh, _ = q.shape
     qp = _dense(q, dev, torch.bfloat16, "q")
     if out is None:
-        out = torch.empty((B, nh, c), dtype=torch.bfloat16, device=q.device)
+        out = _like(q)
     if ws is None:
         if dev == torch._C._cuda_getDevice():
             need = lib().csa_kv4_decode_workspace(nh, nkv, c)
@@ -692,7 +697,7 @@ def _table(table: torch.Tensor, out: Optional[torch.Tensor]):
         raise ValueError("table must be an int32 [rows, max_blocks] tensor")
     dev = _device(table)
     if out is None:
-        out = torch.empty(table.shape, dtype=torch.int32, device=table.device)
+        out = _like(table)
     elif out.shape != table.shape:
         raise ValueError("table_out must be like table")
     return dev, _dense(table, dev, torch.int32, "table"), *table.shape, \
@@ -707,7 +712,7 @@ def csa_blocks_fork(table, src, dst, tokens, fresh, block_tokens: int = 128,
     csa_blocks_copy, once per cache) are -1 where there is nothing to copy."""
     dev, tp, rows, mb, op, out = _table(table, table_out)
     n = src.numel()
-    cs, cd = torch.empty((2, n), dtype=torch.int32, device=table.device)
+    cs, cd = table.new_empty((2, n)).unbind()
     i32 = torch.int32
     _call(lib().csa_blocks_fork, dev, tp, rows, mb, _dense(src, dev, i32, "src"),
           _dense(dst, dev, i32, "dst", n), _dense(tokens, dev, torch.int64, "tokens", n),
@@ -720,8 +725,7 @@ def csa_blocks_free(table, seqs, num_blocks: int, table_out: Optional[torch.Tens
     nfreed): the blocks no row names any more, ascending (int32 [num_blocks],
     -1 padded), and how many (int32 [1])."""
     dev, tp, rows, mb, op, out = _table(table, table_out)
-    freed = torch.empty(num_blocks, dtype=torch.int32, device=table.device)
-    n = torch.empty(1, dtype=torch.int32, device=table.device)
+    freed, n = table.new_empty(num_blocks), table.new_empty(1)
     _call(lib().csa_blocks_free, dev, tp, rows, mb, num_blocks,
           _dense(seqs, dev, torch.int32, "seqs"), seqs.numel(), op, freed.data_ptr(), n.data_ptr())
     return out, freed, n
@@ -733,8 +737,8 @@ def csa_blocks_compact(table, num_blocks: int, table_out: Optional[torch.Tensor]
     csa_blocks_copy with count=counts, once per cache) and counts = [moves,
     blocks in use]."""
     dev, tp, rows, mb, op, out = _table(table, table_out)
-    cs, cd = torch.empty((2, num_blocks), dtype=torch.int32, device=table.device)
-    counts = torch.empty(2, dtype=torch.int32, device=table.device)
+    cs, cd = table.new_empty((2, num_blocks)).unbind()
+    counts = table.new_empty(2)
     _call(lib().csa_blocks_compact, dev, tp, rows, mb, num_blocks, op, cs.data_ptr(),
           cd.data_ptr(), counts.data_ptr())
     return out, cs, cd, counts

@@ -441,9 +441,10 @@ extern "C" csa_status csa_qk_norm_rope(const void* q, int64_t q_stride, const vo
   }
   a.end0 = ends[0]; a.end1 = ends[1]; a.end2 = ends[2];
   Turns turns;
+  const double log_base = log2((double)p->rope_base);
   for (int j = 0; j < p->rope_dims / 2; ++j)
     turns.f[j] = (uint64_t)(0x1p64 / 6.283185307179586476925286766559 *
-                            exp2(-2.0 * j / p->rope_dims * log2((double)p->rope_base)));
+                            exp2(-2.0 * j / p->rope_dims * log_base));
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t r;
   const bool wide = c % 16 == 0 && (!p->halves || p->rope_dims % 16 == 0);
