@@ -56,9 +56,9 @@ __device__ __forceinline__ float row_scale(uint32_t E) {
   return __uint_as_float(E == 255u ? 0x7fc00000u : E << 23);
 }
 
-struct Quant8 {
-  uint32_t codes;  // nibble j = value j
-  uint32_t scale;  // E4M3 of the 16-value group (both lanes of the pair hold it)
+struct Quant16 {
+  uint32_t codes[2];  // nibble j of word w: value 8 w + j
+  uint32_t scale;     // E4M3 of the group
   uint32_t E;
 };
 
@@ -102,9 +102,8 @@ struct Raw8<float> {
   __device__ float2 pair(int i) const { return make_float2(w[2 * i], w[2 * i + 1]); }
 };
 
-// Quantises 8 values of a row spread over `lanes` neighbouring lanes (8
-// values each, lane pairs (2 i, 2 i + 1) forming a group of 16).  Every lane of
-// the warp calls it.
+// Quantises a group of 16 values of a row spread over `lanes` neighbouring
+// lanes, a group each.  Every lane of the warp calls it.
 //
 // No division per value.  bf16: the quotient is a tie k + 1/2 exactly or at
 // least 2^-10 away from one, and x times an approximate reciprocal is within
@@ -115,15 +114,14 @@ struct Raw8<float> {
 // quotient.  A code can lie beyond 7 only for a subnormal s; such groups, and
 // rows near the ends of fp32's range, divide and clamp.
 template <typename T>
-__device__ __forceinline__ Quant8 quantise8(const Raw8<T>& raw, int lanes) {
-  uint32_t a = raw.top();
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+__device__ __forceinline__ Quant16 quantise16(const Raw8<T> (&raw)[2], int lanes) {
+  const uint32_t a = max(raw[0].top(), raw[1].top());
   uint32_t top = a;
-  for (int off = lanes >> 1; off > 1; off >>= 1)
+  for (int off = lanes >> 1; off > 0; off >>= 1)
     top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
   const int ex = (int)(top >> 23);
-  Quant8 q;
-  q.codes = 0x88888888u;
+  Quant16 q;
+  q.codes[0] = q.codes[1] = 0x88888888u;
   q.scale = 0;
   q.E = 255;
   if (ex == 255) return q;
@@ -136,36 +134,40 @@ __device__ __forceinline__ Quant8 quantise8(const Raw8<T>& raw, int lanes) {
   const float step = e4m3_value((uint8_t)q.scale) * __uint_as_float(q.E << 23);
   if (step == 0.f) return q;
   if (q.scale >= 8 && q.E > 24 && q.E < 230) {
-    uint32_t acc = 0;
-    if (Raw8<T>::kFewBits) {
-      float inv;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
-      const float2 inv2 = make_float2(inv, inv);
+    float inv;
+    if (Raw8<T>::kFewBits) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+    else inv = __frcp_rn(step);
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t acc = 0;
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
-        const float2 x = add2(fma2(raw.pair(i), inv2, make_float2(6144.f, 6144.f)),
-                              make_float2(12576776.f, 12576776.f));  // 0x4b400000 + code + 8
+        const float2 v = raw[w].pair(i);
+        float2 x;  // 0x4b400000 + code + 8
+        if (Raw8<T>::kFewBits) {
+          x = add2(fma2(v, inv2, make_float2(6144.f, 6144.f)), make_float2(12576776.f, 12576776.f));
+        } else {
+          const float t = v.x * inv, s = v.y * inv;
+          x = make_float2(fmaf(fmaf(-t, step, v.x), inv, t) + 12582920.f,
+                          fmaf(fmaf(-s, step, v.y), inv, s) + 12582920.f);
+        }
         acc = acc * 16u + __float_as_uint(x.y);
         acc = acc * 16u + __float_as_uint(x.x);
       }
-    } else {
-      const float inv = __frcp_rn(step);
-#pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        const float2 v2 = raw.pair(i >> 1);
-        const float v = i & 1 ? v2.y : v2.x, t = v * inv;
-        acc = acc * 16u + __float_as_uint(fmaf(fmaf(-t, step, v), inv, t) + 12582920.f);
-      }
+      q.codes[w] = acc - 0x3f400000u;  // 0x4b400000 (1 + 16 + 16^2 + ...) mod 2^32
     }
-    q.codes = acc - 0x3f400000u;  // 0x4b400000 (1 + 16 + 16^2 + ...) mod 2^32
     return q;
   }
-  q.codes = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 v2 = raw.pair(i >> 1);
-    const float x = rintf(__fdiv_rn(i & 1 ? v2.y : v2.x, step));
-    q.codes |= (uint32_t)((int)fminf(fmaxf(x, -7.f), 7.f) + 8) << (4 * i);
+  for (int w = 0; w < 2; ++w) {
+    q.codes[w] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = raw[w].pair(i >> 1);
+      const float x = rintf(__fdiv_rn(i & 1 ? v.y : v.x, step));
+      q.codes[w] |= (uint32_t)((int)fminf(fmaxf(x, -7.f), 7.f) + 8) << (4 * i);
+    }
   }
   return q;
 }
@@ -206,13 +208,15 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint3
 
 // Where a lane's part of a row lies in an image: eight dims from 8 sub of a
 // key (is_v = 0) or value row.  For token u = 4 t + 2 h + b every offset is
-// base + h X + t Y + b Z: the codes' two halves lie `half` bytes apart.
+// base + h X + t Y + b Z: the codes' two halves lie `half` bytes apart, and
+// those of the eight dims after an even sub's `next` bytes on.
 template <int C>
 struct LanePart {
-  int codes, half, code_t, code_b, scale, scale_h, scale_t, scale_b, exp;
+  int codes, half, next, code_t, code_b, scale, scale_h, scale_t, scale_b, exp;
   __device__ __forceinline__ LanePart(bool is_v, int sub)
       : codes(is_v ? off_v(C) + v_pair(C, 0, sub * 8) : sub * 4),
         half(is_v ? 4 : 2),
+        next(is_v ? (C == 128 ? 8 : 32) : 4),
         code_t(is_v ? C / 8 : C),
         code_b(is_v ? 2 : C / 2),
         scale(is_v ? off_vs(C) + (sub >> 1) * 16 : off_ks(C) + (sub >> 1)),

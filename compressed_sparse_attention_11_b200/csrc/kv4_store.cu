@@ -1,18 +1,19 @@
 // Rows into the paged 4-bit key/value cache (kv4.cuh: the format) and back.
 //
-// HBM-bound: a bf16 row pair is 4 c bytes in and 1.14 c bytes out.  A warp
-// takes one 16-token image of one (sequence, head): c / 8 lanes hold a row (8
-// values, one 16-byte load each), so at c = 128 the K row and the V row of a
-// token are one warp-wide step, at c = 64 those of two tokens.  An image
+// HBM-bound by its bytes: a bf16 row pair is 4 c bytes in and 1.14 c bytes
+// out.  A warp takes one 16-token image of one (sequence, head).  Storing, a
+// lane holds a group of 16 values (so its scale needs no other lane), and a
+// warp step is the K and V rows of two tokens at c = 128, of four at c = 64;
+// fetching, a lane holds 8 values, whose 16 bytes are one store.  An image
 // that the call covers whole is built in shared memory and written with
 // 16-byte stores; the rows of a partly covered one (the ends of the range;
 // the single token of a decode step) are written in place, only their own
-// bytes.  Bound by instructions: the store issues 128 a lane for eight values
-// (load, row and group maxima by shuffles, E4M3 there and back, four paired
-// fmas and adds, eight shifts into the code word, four small stores), 65 % of
-// the issue slots; the number of rows in flight (4, 8), warps a block (2, 4, 8)
-// and residency (8 to 12 blocks an SM) change nothing.  24 400 tokens of 8 heads,
-// c = 128, bf16: store 38 us (100 MB in, 27 out), fetch 28 us.
+// bytes.  Bound by instructions: the store issues 200 a lane for 16 values
+// (loads, maxima, E4M3 there and back, paired fmas and adds, 16 shifts into the
+// code words, six small stores), 60 % of the issue slots; with 8 values a lane
+// it took 38 us where this takes 33.  Rows in flight (2, 4), warps a block (2,
+// 4) and residency change nothing.  24 400 tokens of 8 heads, c = 128, bf16:
+// store 33 us (100 MB in, 27 out), fetch 27 us.
 #include "api_check.h"
 #include "common.cuh"
 #include "kv4.cuh"
@@ -48,7 +49,7 @@ template <typename T, int C>
 __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const T* __restrict__ k,
                                                                 const T* __restrict__ v,
                                                                 const Kv4Rows a) {
-  constexpr int L = C / 8;        // lanes per row
+  constexpr int L = C / 16;       // lanes per row
   constexpr int TS = 32 / (2 * L);  // tokens per warp step
   __shared__ __align__(16) uint8_t img[kWarps][kv4::tile_bytes(C)];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -69,29 +70,35 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_store_kernel(const T* __restr
   const bool is_v = lane % (2 * L) >= L;
   const int sub = lane % L, ul = lane / (2 * L);
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const T* src = (is_v ? v : k) + (b * a.n + tile * 16 - p0 + ul) * stride + h * C + sub * 8;
-  const kv4::LanePart<C> part(is_v, sub);
-  constexpr int U = sizeof(T) == 2 ? 8 : 4;  // rows in flight
+  const T* src = (is_v ? v : k) + (b * a.n + tile * 16 - p0 + ul) * stride + h * C + sub * 16;
+  const kv4::LanePart<C> part(is_v, 2 * sub);
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // rows in flight
 #pragma unroll
   for (int s0 = 0; s0 < 16; s0 += TS * U) {
     if (s0 + TS * U <= lo || s0 >= hi) continue;
-    kv4::Raw8<T> raw[U];
+    kv4::Raw8<T> raw[U][2];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int s = s0 + i * TS, u = s + ul;
-      raw[i].clear();
-      if (u >= lo && u < hi) raw[i].load(src + s * stride);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        raw[i][w].clear();
+        if (u >= lo && u < hi) raw[i][w].load(src + s * stride + 8 * w);
+      }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int s = s0 + i * TS, u = s + ul;
       if (s + TS <= lo || s >= hi) continue;
-      const kv4::Quant8 q = kv4::quantise8(raw[i], L);
+      const kv4::Quant16 q = kv4::quantise16(raw[i], L);
       if (u < lo || u >= hi) continue;
       uint8_t* c = to + part.code_at(u);
-      *reinterpret_cast<uint16_t*>(c) = (uint16_t)q.codes;
-      *reinterpret_cast<uint16_t*>(c + part.half) = (uint16_t)(q.codes >> 16);
-      if ((sub & 1) == 0) to[part.scale_at(u)] = (uint8_t)q.scale;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        *reinterpret_cast<uint16_t*>(c + w * part.next) = (uint16_t)q.codes[w];
+        *reinterpret_cast<uint16_t*>(c + w * part.next + part.half) = (uint16_t)(q.codes[w] >> 16);
+      }
+      to[part.scale_at(u)] = (uint8_t)q.scale;
       if (sub == 0) to[part.exp_at(u)] = (uint8_t)q.E;
     }
   }
