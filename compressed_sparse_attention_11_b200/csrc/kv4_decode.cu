@@ -705,10 +705,11 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
   const int G = (int)min((int64_t)grid, U);
   const int64_t u0 = (int64_t)before * HV + (int64_t)hv * nu, u1 = u0 + nu;
   const int i0 = nu > 0 ? cta_of(U, G, u0) : 0, i1 = nu > 0 ? cta_of(U, G, u1 - 1) : 0;
-  if (nu > 0 && i0 == i1) return;  // written by the CTA itself
   // (the positions above are older than the kernel before, which let this one
-  // start only after its own wait)
+  // start only after its own wait).  Blocks with nothing to merge wait as well:
+  // what follows in the stream is ordered behind this kernel alone.
   pdl_wait();
+  if (nu > 0 && i0 == i1) return;  // written by the CTA itself
   for (int e = threadIdx.x; e < F::kHeads * (C / 4); e += 256) {
     const int hl = e / (C / 4), d = (e % (C / 4)) * 4;
     if (h0 + hl >= a.group) continue;

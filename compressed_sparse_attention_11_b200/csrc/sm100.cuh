@@ -125,11 +125,19 @@ __device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity,
 // ---- programmatic dependent launch -------------------------------------------
 // A kernel launched with programmatic stream serialization may start while
 // the previous kernel in the stream is still running.  pdl_wait() blocks until
-// that kernel has completed and its writes are visible; every kernel here
-// reads and writes global memory only after it, and calls pdl_trigger()
-// (allowing the next kernel to be scheduled) only after it, so at most two
-// neighbouring kernels overlap and only in their set-up.  Without the launch
-// attribute both are no-ops.
+// that kernel has completed and its writes are visible.  Three rules:
+//   - Every block waits before it exits, whether it has work or not: the next
+//     kernel is ordered behind this one only, so a grid that ended without
+//     waiting would leave the kernel before it running unordered.  (The
+//     selecting decode attention waits for the indexer's published tile
+//     counts in its place, which the indexer raises after its last access.)
+//   - pdl_trigger() (allowing the next kernel to be scheduled) comes only after
+//     the wait, so at most two neighbouring kernels overlap.
+//   - Before the wait a kernel reads no global memory but the inputs of the
+//     call that its own call's kernel before it does not write (positions):
+//     that kernel was let past its wait, so what wrote them has completed.
+//     It writes none.
+// Without the launch attribute both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
