@@ -484,23 +484,34 @@ def _tokens_view(x: torch.Tensor, name: str):
     return tokens, (step if tokens > 1 else heads * c)
 
 
+def _per_head(gamma: torch.Tensor, heads: int, c: int, name: str) -> int:
+    """0 for a weight [c], 1 for [heads, c]."""
+    shape = gamma.shape
+    if shape == (c,):
+        return 0
+    if shape == (heads, c):
+        return 1
+    raise ValueError(f"{name} must be [c] or [heads, c]")
+
+
 def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EPS,
                      rope_dims: int = 64, rope_base: float = ROPE_BASE, halves: bool = False,
                      sections=None, q_out: Optional[torch.Tensor] = None,
                      k_out: Optional[torch.Tensor] = None):
     """RMSNorm (weight [c], or [heads, c] for one per head; None: no norm) and
     rotation of the trailing dims of q [..., nh, c] and k [..., nkv, c] in one
-    pass; either may be None.  ``pos``: int64 [...] as the leading dims, or
-    [axes, ...] with ``sections`` = the pairs of each axis.  q and k may be
-    views with one token stride (of a packed projection); q_out and k_out may
-    be q and k.  Returns (q_out, k_out)."""
+    pass; either may be None.  ``pos``: int64 [...] as the leading dims (or
+    these flattened), or [axes, ...] with ``sections`` = the pairs of each
+    axis.  q and k may be views with one token stride (of a packed
+    projection); q_out and k_out may be q and k.  Returns (q_out, k_out)."""
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
     dev, dt, c, dtype = _device(ref), _dt(ref), ref.shape[-1], ref.dtype
     qp = kp = qop = kop = qg = kg = None
     qs = ks = qos = kos = nh = nkv = 0
-    tokens = per_head = None
+    per_head = None
+    lead = ref.shape[:-2]
     if q is not None:
         nh = q.shape[-2]
         tokens, qs = _tokens_view(q, "q")
@@ -512,15 +523,13 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
             qos = _tokens_view(q_out, "q_out")[1]
         qp, qop = q.data_ptr(), q_out.data_ptr()
         if q_gamma is not None:
-            per_head = q_gamma.dim()
-            qg = _dense(q_gamma, dev, torch.float32, "q_gamma", c if per_head == 1 else nh * c)
+            qg = _dense(q_gamma, dev, torch.float32, "q_gamma")
+            per_head = _per_head(q_gamma, nh, c, "q_gamma")
     if k is not None:
         nkv = k.shape[-2]
-        n, ks = _tokens_view(k, "k")
-        if n != (n if tokens is None else tokens) or k.dtype != dtype or k.get_device() != dev \
-                or k.shape[-1] != c:
-            raise ValueError("q and k must have the same tokens, head dim, dtype and device")
-        tokens = n
+        tokens, ks = _tokens_view(k, "k")
+        if k.shape[:-2] != lead or k.dtype != dtype or k.get_device() != dev or k.shape[-1] != c:
+            raise ValueError("q and k must have the same leading dims, head dim, dtype and device")
         if k_out is None:
             k_out, kos = _like(k), nkv * c
         else:
@@ -529,11 +538,12 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
             kos = _tokens_view(k_out, "k_out")[1]
         kp, kop = k.data_ptr(), k_out.data_ptr()
         if k_gamma is not None:
-            if per_head not in (None, k_gamma.dim()):
+            kg = _dense(k_gamma, dev, torch.float32, "k_gamma")
+            one = _per_head(k_gamma, nkv, c, "k_gamma")
+            if per_head is not None and per_head != one:
                 raise ValueError("q_gamma and k_gamma must both be [c] or both be [heads, c]")
-            per_head = k_gamma.dim()
-            kg = _dense(k_gamma, dev, torch.float32, "k_gamma", c if per_head == 1 else nkv * c)
-    p = QkRope(qg, kg, 1 if per_head == 2 else 0, eps, rope_dims, rope_base, 1 if halves else 0)
+            per_head = one
+    p = QkRope(qg, kg, per_head or 0, eps, rope_dims, rope_base, 1 if halves else 0)
     if sections is None:
         p.axes, p.sections[0] = 1, rope_dims // 2
     else:
@@ -542,7 +552,15 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
             raise ValueError("1 to 4 sections")
         for i, n in enumerate(sections):
             p.sections[i] = n
-    pp = _dense(pos, dev, torch.int64, "pos", p.axes * tokens) if rope_dims else None
+    pp = None
+    if rope_dims and pos is not None:
+        pp = _dense(pos, dev, torch.int64, "pos")
+        shape = pos.shape
+        if p.axes > 1 or shape != lead:
+            one = shape[1:] if shape[:1] == (p.axes,) else shape if p.axes == 1 else None
+            if one != lead and one != (tokens,):
+                raise ValueError("pos must have the leading dims of q and k, behind one of the axes "
+                                 "where there are sections")
     _call(lib().csa_qk_norm_rope, dev, qp, qs, kp, ks, tokens, nh, nkv, c, pp, ctypes.byref(p), dt,
           qop, qos, kop, kos)
     return q_out if q is not None else None, k_out if k is not None else None
