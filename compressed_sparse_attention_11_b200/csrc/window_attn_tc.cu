@@ -37,10 +37,18 @@
 // is full).  2 x 8192 tokens, 32 heads over 8, W = 1024, 4 first tokens,
 // C = 128: 308 us, 840 TFLOP/s.
 //
-// A value row that is not finite where a query's mask hides it would still
-// reach that query through 0 x inf in the second product.  The epilogue sees
-// that as an output that is not finite and recomputes the row from global
-// memory over its visible keys alone; no other row pays for it.
+// A value that is not finite would reach the queries that a mask hides it from
+// through 0 x inf in the second product.  Hidden keys exist only in the edge
+// tiles of a query tile (the last ones, the lower end of the window, the first
+// tokens).  Two warps that are idle otherwise look through the values of those
+// before the product takes them, and set such values to zero; from then on the
+// CTA's epilogues look them up again in global memory and add them to the rows
+// that see them.  In the tiles between, every row sees every key, and the
+// product itself gives the right infinity or NaN.  So the time is bounded by the
+// edge tiles, whatever the window (8192 tokens, 32 over 8 heads x 128, W = 1024:
+// 168 us; 381 with one infinite value, 2.5 ms where every value is NaN).  Finite
+// values pay nothing (342 us for 2 x 8192 tokens, sustained, with the scan and
+// without); a wait of the MMA warp for the copy beside the one for the scan cost 12.
 #include "api_check.h"
 #include "common.cuh"
 #include "launch.h"
@@ -58,7 +66,8 @@ constexpr int kSlab = kRows * 128;  // 16 KB: 128 rows x 64 dims
 constexpr int kStages = 2;
 constexpr int kSoftWarps = 8;  // two warpgroups
 constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + 1;
-constexpr int kThreads = (kSoftWarps + 4) * 32;  // two idle warps fill the last warpgroup
+constexpr int kScanWarp = kSoftWarps + 2, kScanWarps = 2;
+constexpr int kThreads = (kScanWarp + kScanWarps) * 32;
 // Registers a thread: 168 x 384 at launch, moved between the warpgroups:
 // 208 x 256 + 88 x 128 = 168 x 384.
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
@@ -93,11 +102,12 @@ struct Cfg {
 struct __align__(8) WinBars {
   uint64_t q_full[2], q_free[2];
   uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+  uint64_t v_seen[kStages];  // the values have been looked through
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t wg[2];  // bounded barrier of the four warps of a warpgroup
   uint64_t drain;
   uint32_t tmem_base;
-  uint32_t odd[2];  // a row of the query tile has an output that is not finite
+  uint32_t odd;  // values of some edge tile were not finite and are zeros in shared memory
 };
 
 // One pair of query tiles and its list of key tiles.
@@ -156,36 +166,78 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// One row again in fp32, the lanes of the warp sharing the dims.
+// Whether a mask hides a key of tile tj from a row of query tile q.
+__device__ __forceinline__ bool edge_tile(const WinArgs& a, const Job& j, int q, int tj) {
+  const int ta = j.t0 + q * a.tt, tb = min(ta + a.tt - 1, j.t1), base = j.base(tj);
+  return base + kKeys - 1 > ta || tb - a.window + 1 > base;
+}
+// Whether its values are looked through: an edge tile of a query tile that needs it.
+__device__ __forceinline__ bool scanned(const WinArgs& a, const Job& j, const Need (&need)[2], int tj) {
+  return (need[0].has(tj) && edge_tile(a, j, 0, tj)) || (need[1].has(tj) && edge_tile(a, j, 1, tj));
+}
+// Largest magnitudes of the upper and lower bf16 values of four words.
+__device__ __forceinline__ uint32_t tops(const uint4& x) {
+  constexpr uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+}
+__device__ __forceinline__ bool not_finite(uint32_t top) {
+  return top >= 0x7f800000u || (top & 0xffffu) >= 0x7f80u;
+}
+// (rare) The values of the scanned tiles that are not finite, added to the
+// output of this thread's row (position t) where the row sees them.  Every lane
+// looks at 32 dims of one key; then all lanes take the keys that have such a
+// value in turn.
 template <int C>
-__device__ __noinline__ void exact_row(const WinArgs& a, const Job& j, int i, int head, float m,
-                                       float inv, __nv_bfloat16* out) {
+__device__ __noinline__ void add_odd_values(const WinArgs& a, const Job& j, int q, int t, uint32_t o_addr) {
   const int lane = threadIdx.x & 31;
-  constexpr int E = C / 32;
-  const __nv_bfloat16* q = a.q + ((int64_t)j.b * a.nq + i) * a.q_stride + (int64_t)head * C;
-  float qv[E], acc[E];
+  const Need need[2] = {need_of(a, j, 0), need_of(a, j, 1)};
+  for (int tj = 0; tj < j.tiles; ++tj) {
+    if (!need[q].has(tj) || !scanned(a, j, need, tj)) continue;
+#pragma unroll 1
+    for (int d = 0; d < C; d += 32) {
+      uint32_t o[32];
+      tmem_ld32(o_addr + d, o);
+      tmem_ld_wait();
+#pragma unroll 1
+      for (int i0 = 0; i0 < kKeys; i0 += 32) {
+        const int col = tj * kKeys + i0 + lane;
+        const int u = col < j.f8 ? col : j.klo + col - j.f8;
+        uint32_t y[16];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __bfloat162float(q[lane + 32 * e]);
-    acc[e] = 0.f;
+        for (int k = 0; k < 16; ++k) y[k] = 0u;
+        if (u < a.nk && !(col < j.f8 && u >= a.first)) {
+          const uint4* x = reinterpret_cast<const uint4*>(
+              a.v + ((int64_t)j.b * a.nk + u) * a.v_stride + (int64_t)j.h * C + d);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 z = __ldg(x + k);
+            y[4 * k] = z.x; y[4 * k + 1] = z.y; y[4 * k + 2] = z.z; y[4 * k + 3] = z.w;
+          }
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = __vmaxu2(top, y[k] & 0x7fff7fffu);
+        unsigned todo = __ballot_sync(0xffffffffu, not_finite(top));
+        while (todo) {
+          const int from = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int uu = __shfl_sync(0xffffffffu, u, from);
+          const bool sees = uu <= t && (uu > t - a.window || uu < a.first);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t w = __shfl_sync(0xffffffffu, y[k], from);
+            const uint32_t lo = w << 16, hi = w & 0xffff0000u;
+            if (sees && (lo & 0x7f800000u) == 0x7f800000u)
+              o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) + __uint_as_float(lo));
+            if (sees && (hi & 0x7f800000u) == 0x7f800000u)
+              o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) + __uint_as_float(hi));
+          }
+        }
+      }
+      tmem_st32(o_addr + d, o);
+      tmem_st_wait();
+    }
   }
-  const int t = a.nk - a.nq + i;
-  for (int u = 0; u <= t; ++u) {
-    if (u >= a.first && u <= t - a.window) u = t - a.window + 1;  // on to the window
-    const int64_t row = (int64_t)j.b * a.nk + u;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      s = fmaf(qv[e], __bfloat162float(a.k[row * a.k_stride + (int64_t)j.h * C + lane + 32 * e]), s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float p = ex2(fmaf(a.neg ? -s : s, a.qs, -m));
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      acc[e] = fmaf(p, __bfloat162float(a.v[row * a.v_stride + (int64_t)j.h * C + lane + 32 * e]), acc[e]);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
 template <int C>
@@ -217,9 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
       mbar_init(&bar->k_free[i], 1);
       mbar_init(&bar->v_full[i], 1);
       mbar_init(&bar->v_free[i], 1);
+      mbar_init(&bar->v_seen[i], kScanWarps);
     }
     mbar_init(&bar->drain, 1);
-    bar->odd[0] = bar->odd[1] = 0;
+    bar->odd = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -321,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     // weights of key tile k (its values in stage k % kStages) into O_q
     auto issue_pv = [&](int q, int k, bool first, bool last) -> bool {
       const int st = k % kStages;
-      if (!mbar_wait(&bar->v_full[st], (uint32_t)((k / kStages) & 1), err)) return false;
+      if (!mbar_wait(&bar->v_seen[st], (uint32_t)((k / kStages) & 1), err)) return false;
       // the first P.V of a query tile overwrites O: the epilogue before has read it
       if (first && jobs[q] > 0 && !mbar_wait(&bar->o_free[q], (uint32_t)((jobs[q] - 1) & 1), err))
         return false;
@@ -377,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
         if (tj < jb.tiles) {
           // (a tile that no row needs was loaded all the same)
           if (!have_k && !(ok = mbar_wait(&bar->k_full[st], (uint32_t)((n / kStages) & 1), err) &&
-                                mbar_wait(&bar->v_full[st], (uint32_t)((n / kStages) & 1), err)))
+                                mbar_wait(&bar->v_seen[st], (uint32_t)((n / kStages) & 1), err)))
             break;
           if (lane == 0) mma_commit(&bar->k_free[st]);
           ++n;
@@ -388,6 +441,46 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     if (lane == 0) mma_commit(&bar->drain);
     __syncwarp();
     mbar_wait(&bar->drain, 0, err, false);
+  } else {
+    // =================== values of the edge tiles, a half each ====================
+    // (the MMA warp waits for every tile's scan before it frees the stage, so a
+    // scan is never a phase behind)
+    constexpr int kPer = F::kTileBytes / 16 / kScanWarps / 32;
+    int n = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
+      const Job jb = job_of(a, w);
+      const Need need[2] = {need_of(a, jb, 0), need_of(a, jb, 1)};
+      for (int tj = 0; tj < jb.tiles; ++tj, ++n) {
+        const int st = n % kStages;
+        if (!(ok = mbar_wait(&bar->v_full[st], (uint32_t)((n / kStages) & 1), err))) break;
+        if (scanned(a, jb, need, tj)) {
+          uint4* x = reinterpret_cast<uint4*>(smem + F::off_v + st * F::kTileBytes) +
+                     (warp - kScanWarp) * kPer * 32 + lane;
+          uint32_t top = 0;
+#pragma unroll 8
+          for (int i = 0; i < kPer; ++i) top = __vmaxu2(top, tops(x[32 * i]));
+          if (__any_sync(0xffffffffu, not_finite(top))) {
+#pragma unroll 1
+            for (int i = 0; i < kPer; ++i) {
+              const uint4 y = x[32 * i];
+              if (!not_finite(tops(y))) continue;
+              uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+                if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
+              }
+              x[32 * i] = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+            if (lane == 0) *(volatile uint32_t*)&bar->odd = 1u;
+          }
+        }
+        fence_proxy_async();  // the MMA warp waits for this scan, not for the copy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->v_seen[st]);
+      }
+    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -494,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
       const float mr = m == kNegInf ? 0.f : m;
       const float z = real && a.sink != nullptr ? a.sink[head] * kLog2e : kNegInf;
       const float inv = 1.f / (l + ex2(z - mr));
-      bool odd = false;  // an output that is not finite
+      if (*(const volatile uint32_t*)&bar->odd != 0) add_odd_values<C>(a, jb, q, t, o_addr);
 #pragma unroll 1
       for (int sl = 0; sl < F::kSlabs; ++sl) {
         uint32_t pk[32];
@@ -506,7 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float x = __uint_as_float(o[e]) * inv, y = __uint_as_float(o[e + 1]) * inv;
-            odd |= !(fabsf(x) <= 3.4028234664e38f) || !(fabsf(y) <= 3.4028234664e38f);
             pk[16 * c + (e >> 1)] = pack_bf16x2(x, y);
           }
         }
@@ -523,28 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
         for (int c = 0; c < 8; ++c)
           *reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) * 16)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        if (odd && real) bar->odd[q] = 1;
         fence_proxy_async();
         if (!(ok = group_sync(&bar->wg[q], wg_phase, err))) break;
         if (row == 0) {
           tma_store_4d(&tm_o, stage, sl * 64, jb.h * a.group, jb.i0 + q * a.tt, jb.b);
           bulk_commit_group();
         }
-      }
-      if (!ok) break;
-      if (bar->odd[q] == 0) continue;
-      // (rare) such rows again, key by key, once the warpgroup's stores are done
-      if (row == 0) bulk_wait_all();
-      if (!(ok = group_sync(&bar->wg[q], wg_phase, err))) break;
-      if (row == 0) bar->odd[q] = 0;
-      unsigned todo = __ballot_sync(0xffffffffu, odd && real);
-      while (todo) {
-        const int r = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int ri = __shfl_sync(0xffffffffu, i, r), rh = __shfl_sync(0xffffffffu, head, r);
-        const float rm = __shfl_sync(0xffffffffu, mr, r), rinv = __shfl_sync(0xffffffffu, inv, r);
-        exact_row<C>(a, jb, ri, rh, rm, rinv,
-                     a.out + (((int64_t)jb.b * a.nq + ri) * a.nh + rh) * C);
       }
     }
     if (row == 0) bulk_wait_all();
