@@ -20,9 +20,21 @@
 // instructions where the bytes take 148).
 // f16's range: a query head is scaled to largest element 1 .. 2 (elements below
 // 2^-14 of it keep an absolute 2^-25), and the second product's weight is
-// w_u = 2^(l_u + E_u - M'), E_u the value row's exponent and M' a running
-// maximum of its own, so that the rows that make up the output have weights
-// near 1 whatever their magnitude.
+// w_u = 2^(l_u + E_u - M'), E_u the value row's exponent and M' a reference of
+// its own, 8 to 15 below the running maximum of l + E, so that the rows with
+// the largest products have weights of 2^8 and more whatever their magnitude.
+// In w's f16 a row with E_u near the maximum's keeps an absolute 2^-33 of the
+// largest softmax weight.  A row whose values are far smaller than the largest
+// ones (E_u more than 5 below M' + 8 - M) could lose a weight that counts in
+// the dims where the large rows hold little: for such rows the remainders
+// w - f16(w) are multiplied as well, scaled by 2^26, 2^52 and 2^78 (with O, in
+// fp32, scaled alike meanwhile), so each weight is off by 2^-11 of itself or
+// 2^-28 of the largest one at most, for rows whose products lie up to 2^90 apart.
+// That path is taken where a warp's two images hold such a row and costs three
+// more second products there: 32 sequences of 24 576 tokens, 64 / 8 heads x 128:
+// 208 us with rows alike, 236 with one row in 4096 2^12 times the others, 310 with
+// every second row 2^-12 of its neighbours.  Rows alike pay 2 % for its presence
+// (208 -> 212 us, sustained).
 // tcgen05 would need the widened rows in shared memory first (16-bit operands
 // of both products through it: four times the cache's bytes), which is more
 // than an SM's share of HBM time allows; mma.sync takes them from registers.
@@ -37,6 +49,7 @@
 // 32 sequences of 16-32 K tokens, 64 / 8 heads x 128, whose bytes alone take
 // 148).  What a CTA covers whole is written out; other pieces go to the
 // workspace (two slots a CTA) and a second kernel merges them.
+#include <cuda_fp16.h>
 #include <limits.h>
 
 #include <type_traits>
@@ -58,6 +71,13 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2;                     // neighbouring images a warp takes at once
 constexpr int kUnitTiles = kPair * kWarps;  // images per unit
 constexpr float kRescaleLog2 = 8.f;
+// Weights of the output: the largest is 2^8 when its reference is set and may
+// grow to 2^15 before the reference moves (f16 ends at 65504).
+constexpr float kTopLog2 = 8.f, kMostLog2 = 15.f;
+// A row whose exponent lies more than 5 below what the reference stands for has
+// its weight's remainder taken along, in steps of 2^26.
+constexpr float kDeepLog2 = 5.f;
+constexpr int kDeepSteps = 3;
 constexpr float kNone = -3e38f;  // running maximum of a head that has seen nothing
 
 struct DecArgs {
@@ -145,6 +165,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// What f16 leaves of a value below its normal range (0 for larger ones, whose
+// 11 bits do).
+__device__ __forceinline__ float f16_rest(float x) {
+  return fabsf(x) < 0x1p-14f ? x - __half2float(__float2half_rn(x)) : 0.f;
+}
+
 // f16 pairs kept in registers (a logic instruction takes one immediate, the
 // mask; the others would be fetched anew at each use).
 struct Bases {
@@ -185,11 +211,14 @@ __device__ __forceinline__ void widen4(uint32_t w, const ScalePair& s, const Bas
 }
 
 // A piece's state per head: running maximum M of the logits (log2 units), sum
-// L of 2^(l - M), and the reference MV of the output's weights.
-__device__ __forceinline__ float out_factor(float M, float L, float MV, const float* sink, int head) {
-  if (M == kNone) return L == 0.f ? 0.f : L;  // nothing seen: zeros (a NaN sum stays one)
+// L of 2^(l - M), and the reference MV of the output's weights.  The output is
+// O times both factors (their product can leave fp32's range where the output
+// does not).
+__device__ __forceinline__ float2 out_factors(float M, float L, float MV, const float* sink, int head) {
+  if (M == kNone) return make_float2(L == 0.f ? 0.f : L, 1.f);  // nothing seen: zeros (a NaN sum stays one)
   const float den = L + (sink != nullptr ? ex2(sink[head] * kLog2e - M) : 0.f);
-  return ex2(MV - M - (127.f - 8.f)) / den;  // E's bias, and the scales' 2^-8
+  const float f = ex2(0.5f * (MV - M - (127.f - 8.f)));  // E's bias, and the scales' 2^-8
+  return make_float2(f / den, f);
 }
 
 template <int C, int NT>
@@ -416,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
     }
     float o[NT][MT][4];
     float m[NT][2], l[NT][2], mv[NT][2];
+    float deep = kNone;  // rows with a smaller E: their weights' remainders count
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       m[t][0] = m[t][1] = mv[t][0] = mv[t][1] = kNone;
@@ -472,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
         }
       }
       // ---- online softmax: l, and l + E of the value row ----------------------
-      float lv[N][NT][4];
+      float lv[N][NT][4], ev[N][2];
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -480,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
           const float kr = __uint_as_float((ex[n][r] & 255u) << 23);
           // E as a float; infinite for a row that is not finite (0 w then makes NaN)
           const float ve = ex[n][r] >= 0xff00u ? __int_as_float(0x7f800000) : (float)(ex[n][r] >> 8);
+          ev[n][r] = ve;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const float2 s = mul2(mul2(make_float2(sc[n][t][2 * r], sc[n][t][2 * r + 1]), make_float2(kr, kr)),
@@ -505,7 +536,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
           }
         }
       float tm[NT][2], tv[NT][2];
-      bool grow = false;
+      bool grow = false, low = false;
+#pragma unroll
+      for (int n = 0; n < N; ++n) low |= fminf(ev[n][0], ev[n][1]) < deep;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -516,51 +549,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
             tm[t][e] = fmaxf(tm[t][e], fmaxf(sc[N - 1][t][e], sc[N - 1][t][2 + e]));
             tv[t][e] = fmaxf(tv[t][e], fmaxf(lv[N - 1][t][e], lv[N - 1][t][2 + e]));
           }
-          grow |= tm[t][e] > m[t][e] + kRescaleLog2 || tv[t][e] > mv[t][e] + kRescaleLog2;
+          grow |= tm[t][e] > m[t][e] + kRescaleLog2 || tv[t][e] > mv[t][e] + kMostLog2;
         }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = tm[t][e], y = tv[t][e];
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) {
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
-            }
-            x = fmaxf(x, m[t][e]);
-            y = fmaxf(y, mv[t][e]);
-            if (x > m[t][e]) l[t][e] *= ex2(m[t][e] - x);
-            m[t][e] = x;
-            if (y > mv[t][e]) {
-              const float f = ex2(mv[t][e] - y);
-              mv[t][e] = y;
-#pragma unroll
-              for (int k = 0; k < MT; ++k) {
-                o[t][k][e] *= f;
-                o[t][k][2 + e] *= f;
-              }
-            }
-          }
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            l[t][e] += ex2(sc[n][t][e] - m[t][e]) + ex2(sc[n][t][2 + e] - m[t][e]);
-            w[e] = ex2(lv[n][t][e] - mv[t][e]);
-            w[2 + e] = ex2(lv[n][t][2 + e] - mv[t][e]);
-          }
-          pb[t][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-          pb[t][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-        }
-        // ---- O^T += V^T P^T --------------------------------------------------
-        const uint8_t* im = im0 + n * F::kTB;
+      // ---- O^T += V^T P^T of one image ------------------------------------------
+      auto second_product = [&](const uint8_t* im, const uint32_t (&pb)[NT][2]) {
         const uint8_t* vim = im + kv4::off_v(C) + gid * 4 * D + tig * D;
         // (bytes of rows never written may be anything: kept finite, their weight is 0)
         const uint32_t vs = 0x7f7f7f7fu & *reinterpret_cast<const uint32_t*>(
@@ -589,6 +581,110 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
             mma_16816(o[t][2 * w + 1], a0[2], a0[3], a1[2], a1[3], pb[t][0], pb[t][1]);
           }
         }
+      };
+      if (__any_sync(0xffffffffu, grow || low)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = tm[t][e], y = tv[t][e];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+            }
+            x = fmaxf(x, m[t][e]);
+            y = fmaxf(y - kTopLog2, mv[t][e]);
+            if (x > m[t][e]) l[t][e] *= ex2(m[t][e] - x);
+            m[t][e] = x;
+            if (y > mv[t][e]) {
+              const float f = ex2(mv[t][e] - y);
+              mv[t][e] = y;
+#pragma unroll
+              for (int k = 0; k < MT; ++k) {
+                o[t][k][e] *= f;
+                o[t][k][2 + e] *= f;
+              }
+            }
+          }
+        deep = kNone;  // (heads that are not finite have no say)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float d = mv[t][e] - m[t][e] + (kTopLog2 - kDeepLog2);
+            if (d < 512.f) deep = fmaxf(deep, d);
+          }
+#pragma unroll
+        for (int w = 1; w < 4; w <<= 1) deep = fmaxf(deep, __shfl_xor_sync(0xffffffffu, deep, w));
+        // a row that is seen, far below in E, whose weight is an f16 subnormal?
+        low = false;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (ev[n][r] < deep)
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float x = lv[n][t][2 * r + e] - mv[t][e];
+                  low |= x < -14.f && x > -14.f - 26.f * kDeepSteps - 4.f;
+                }
+        if (__any_sync(0xffffffffu, low)) {
+#pragma unroll 1
+          for (int n = 0; n < N; ++n) {
+            float w[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[t][i] = f16_rest(ex2((n == 0 ? lv[0][t][i] : lv[N - 1][t][i]) - mv[t][i & 1]));
+#pragma unroll 1
+            for (int step = 0; step < kDeepSteps; ++step) {
+              uint32_t pb[NT][2];
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int k = 0; k < MT; ++k)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[t][k][i] *= 0x1p26f;
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  x[i] = w[t][i] * 0x1p26f;  // 2 at most
+                  w[t][i] = f16_rest(x[i]);
+                }
+                pb[t][0] = transpose8x8(pack_f16x2(x[0], x[1]));
+                pb[t][1] = transpose8x8(pack_f16x2(x[2], x[3]));
+              }
+              second_product(im0 + n * F::kTB, pb);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int k = 0; k < MT; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[t][k][i] *= 0x1p-78f;
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[t][e] += ex2(sc[n][t][e] - m[t][e]) + ex2(sc[n][t][2 + e] - m[t][e]);
+            w[e] = ex2(lv[n][t][e] - mv[t][e]);
+            w[2 + e] = ex2(lv[n][t][2 + e] - mv[t][e]);
+          }
+          pb[t][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+          pb[t][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+        }
+        second_product(im0 + n * F::kTB, pb);
       }
     };
 
@@ -650,10 +746,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_decode_kernel(c
       if (direct) {
         if (h0 + hl < a.group) {
           const int head = kvh * a.group + h0 + hl;
-          const float inv = out_factor(M, L, MV, a.sink, head);
+          const float2 f = out_factors(M, L, MV, a.sink, head);
           uint2 w;
-          w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-          w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+          w.x = pack_bf16x2(acc.x * f.x * f.y, acc.y * f.x * f.y);
+          w.y = pack_bf16x2(acc.z * f.x * f.y, acc.w * f.x * f.y);
           *reinterpret_cast<uint2*>(a.out + ((int64_t)cur_b * a.nh + head) * C + d) = w;
         }
       } else {
@@ -735,10 +831,10 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant_
         acc.w = acc.w * f0 + y.w * f1;
       }
     }
-    const float inv = out_factor(M, L, MV, a.sink, head);
+    const float2 f = out_factors(M, L, MV, a.sink, head);
     uint2 w;
-    w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    w.x = pack_bf16x2(acc.x * f.x * f.y, acc.y * f.x * f.y);
+    w.y = pack_bf16x2(acc.z * f.x * f.y, acc.w * f.x * f.y);
     *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.nh + head) * C + d) = w;
   }
 }

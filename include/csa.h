@@ -556,10 +556,14 @@ size_t csa_kv4_decode_workspace(int nh, int nkv, int c);
  * int64 [batch]; a negative pos[b] gives zeros), over the cache:
  *   E_b = { u <= pos[b] : u > pos[b] - window or u < first }, window = 0: all;
  * the softmax, sink and heads as csa_window_attn.  A sequence that sees no row
- * gives zeros.  Positions are below 2^31 - 1.  q, out : [batch, nh, c] bf16
- * (within a head, elements of q below 2^-14 of its largest keep an absolute
- * error of 2^-25 of that).  ws: scratch of this call alone
- * until it has finished on the stream. */
+ * gives zeros.  Positions are below 2^31 - 1.  q, out : [batch, nh, c] bf16.
+ * Operands are 16-bit floats, sums fp32: within a head, elements of q below
+ * 2^-14 of its largest keep an absolute error of 2^-25 of that; a softmax
+ * weight is off by at most 2^-11 of itself or 2^-28 of the head's largest,
+ * whatever the sizes of the value rows, as long as a row's weight times its
+ * largest element is more than 2^-90 of the largest such product (below that
+ * it may count as zero).  ws: scratch of this call alone until it has finished
+ * on the stream. */
 csa_status csa_kv4_decode_attn(const csa_kv4_cache* cache, const int64_t* pos, const void* q,
                                int nh, int64_t window, int64_t first, const float* sink,
                                float scale, void* out, void* ws, size_t ws_bytes, void* stream);
