@@ -486,10 +486,10 @@ def _tokens_view(x: torch.Tensor, name: str):
 
 def _per_head(gamma: torch.Tensor, heads: int, c: int, name: str) -> int:
     """0 for a weight [c], 1 for [heads, c]."""
-    shape = gamma.shape
-    if shape == (c,):
+    dims, n = gamma.dim(), gamma.numel()
+    if dims == 1 and n == c:
         return 0
-    if shape == (heads, c):
+    if dims == 2 and n == heads * c and gamma.size(1) == c:
         return 1
     raise ValueError(f"{name} must be [c] or [heads, c]")
 
@@ -507,13 +507,13 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    dev, dt, c, dtype = _device(ref), _dt(ref), ref.shape[-1], ref.dtype
+    dev, dt, dtype, shape = _device(ref), _dt(ref), ref.dtype, tuple(ref.shape)
+    lead, c = shape[:-2], shape[-1]
     qp = kp = qop = kop = qg = kg = None
     qs = ks = qos = kos = nh = nkv = 0
     per_head = None
-    lead = ref.shape[:-2]
     if q is not None:
-        nh = q.shape[-2]
+        nh = shape[-2]
         tokens, qs = _tokens_view(q, "q")
         if q_out is None:
             q_out, qos = _like(q), nh * c
@@ -526,9 +526,10 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
             qg = _dense(q_gamma, dev, torch.float32, "q_gamma")
             per_head = _per_head(q_gamma, nh, c, "q_gamma")
     if k is not None:
-        nkv = k.shape[-2]
+        shape = tuple(k.shape)
+        nkv = shape[-2]
         tokens, ks = _tokens_view(k, "k")
-        if k.shape[:-2] != lead or k.dtype != dtype or k.get_device() != dev or k.shape[-1] != c:
+        if shape[:-2] != lead or shape[-1] != c or k.dtype != dtype or k.get_device() != dev:
             raise ValueError("q and k must have the same leading dims, head dim, dtype and device")
         if k_out is None:
             k_out, kos = _like(k), nkv * c
@@ -544,20 +545,22 @@ def csa_qk_norm_rope(q, k, pos, q_gamma=None, k_gamma=None, eps: float = NORM_EP
                 raise ValueError("q_gamma and k_gamma must both be [c] or both be [heads, c]")
             per_head = one
     p = QkRope(qg, kg, per_head or 0, eps, rope_dims, rope_base, 1 if halves else 0)
+    axes = 1
     if sections is None:
-        p.axes, p.sections[0] = 1, rope_dims // 2
+        p.sections[0] = rope_dims // 2
     else:
-        p.axes = len(sections)
-        if not 1 <= p.axes <= 4:
+        axes = len(sections)
+        if not 1 <= axes <= 4:
             raise ValueError("1 to 4 sections")
         for i, n in enumerate(sections):
             p.sections[i] = n
+    p.axes = axes
     pp = None
     if rope_dims and pos is not None:
         pp = _dense(pos, dev, torch.int64, "pos")
-        shape = pos.shape
-        if p.axes > 1 or shape != lead:
-            one = shape[1:] if shape[:1] == (p.axes,) else shape if p.axes == 1 else None
+        shape = tuple(pos.shape)
+        if axes > 1 or shape != lead:
+            one = shape[1:] if shape[:1] == (axes,) else shape if axes == 1 else None
             if one != lead and one != (tokens,):
                 raise ValueError("pos must have the leading dims of q and k, behind one of the axes "
                                  "where there are sections")
