@@ -171,7 +171,7 @@ __device__ __forceinline__ int prefix_words(const uint32_t* bits, int* pre, int 
 
 // One block of threads: a bitmap of the blocks in shared memory, so no
 // scratch in global memory and one launch (table and lists are read and
-// written once: 64 x 64 entries 5 us, 256 x 256 30, 256 x 4096 0.4 ms; batches
+// written once: 64 x 64 entries 5 us, 256 x 256 30, 256 x 4096 0.34 ms; batches
 // of eight loads before the first use changed nothing).
 // Freed: named by a row in `seqs` and by no other row.
 __global__ void __launch_bounds__(kOneThreads) blocks_free_kernel(

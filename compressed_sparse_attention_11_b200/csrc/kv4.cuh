@@ -110,8 +110,9 @@ struct Raw8<float> {
 // 7.5 2^-23 of it; adding 6144 rounds that sum to a multiple of 2^-11, which
 // restores a tie and moves nothing across one; adding the rest of 1.5 2^23 + 8
 // then rounds to nearest even.  fp32: x times the correctly rounded
-// reciprocal, corrected once by the exact remainder, is the correctly rounded
-// quotient.  A code can lie beyond 7 only for a subnormal s; such groups, and
+// reciprocal, corrected once by the exact remainder (Markstein's method), is the
+// correctly rounded quotient: true of every mantissa of x and every divisor of
+// four significant bits, as all these are (in integers: all 2^23 x 8 cases).  A code can lie beyond 7 only for a subnormal s; such groups, and
 // rows near the ends of fp32's range, divide and clamp.
 template <typename T>
 __device__ __forceinline__ Quant16 quantise16(const Raw8<T> (&raw)[2], int lanes) {
@@ -126,8 +127,8 @@ __device__ __forceinline__ Quant16 quantise16(const Raw8<T> (&raw)[2], int lanes
   q.E = 255;
   if (ex == 255) return q;
   q.E = (uint32_t)max(ex - 10, 1);
-  // a / (7 r), correctly rounded: a / r is exact, the remainder of the first
-  // quotient by 7 too
+  // a / (7 r), correctly rounded likewise: a / r is exact, the remainder of the
+  // first quotient by 7 too
   const float ar = __uint_as_float(a) * __uint_as_float((254u - q.E) << 23);
   const float q0 = ar * (1.f / 7.f);
   q.scale = e4m3_code(fmaf(fmaf(-q0, 7.f, ar), 1.f / 7.f, q0));

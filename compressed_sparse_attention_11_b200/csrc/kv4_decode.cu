@@ -16,8 +16,9 @@
 // s (n - 8) exactly; (x & 0x000f) | 0x6400 is 1024 + n and takes a subtraction
 // and a product; the upper two follow after one shift.  Logic and shifts were
 // the bound with bf16 operands, whose seven mantissa bits want a shift per
-// nibble; now these and the f16 arithmetic weigh about the same (190 us of
-// instructions where the bytes take 148).
+// nibble; now these and the f16 arithmetic weigh about the same (ALU 53 %, FMA
+// 49 %, two thirds of the issue slots: no pipe is full, dependent steps of four
+// warps a scheduler leave the rest).
 // f16's range: a query head is scaled to largest element 1 .. 2 (elements below
 // 2^-14 of it keep an absolute 2^-25), and the second product's weight is
 // w_u = 2^(l_u + E_u - M'), E_u the value row's exponent and M' a reference of
@@ -45,9 +46,9 @@
 // a ring of its own, so no warp waits for another (one ring for the CTA moved
 // the warps in step and took a fifth longer), with its own running maxima, sum
 // and output; the four are merged where a sequence ends or the CTA's share
-// does (four CTAs of four warps on an SM: 197 us; two of eight: 201; times at
-// 32 sequences of 16-32 K tokens, 64 / 8 heads x 128, whose bytes alone take
-// 148).  What a CTA covers whole is written out; other pieces go to the
+// does (four CTAs of four warps on an SM: 197 us in short runs, before the
+// remainders; two of eight: 201; times at 32 sequences of 16-32 K tokens, 64 / 8
+// heads x 128, whose bytes take 140; 212 sustained now).  What a CTA covers whole is written out; other pieces go to the
 // workspace (two slots a CTA) and a second kernel merges them.
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -192,8 +193,7 @@ __device__ __forceinline__ ScalePair scale_pair(uint32_t bytes, uint32_t sel, co
   p.n72 = mul_f16x2(p.s, k.m72);
   return p;
 }
-// (w & kMask) | k in one instruction (left to itself the compiler took two,
-// and the kernel 229 us instead of 201).
+// (w & kMask) | k as one lop3: 201 us, written as two operators 229.
 template <uint32_t kMask>
 __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t k) {
   uint32_t d;

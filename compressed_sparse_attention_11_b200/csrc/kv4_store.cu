@@ -8,12 +8,15 @@
 // that the call covers whole is built in shared memory and written with
 // 16-byte stores; the rows of a partly covered one (the ends of the range;
 // the single token of a decode step) are written in place, only their own
-// bytes.  Bound by instructions: the store issues 200 a lane for 16 values
-// (loads, maxima, E4M3 there and back, paired fmas and adds, 16 shifts into the
-// code words, six small stores), 60 % of the issue slots; with 8 values a lane
-// it took 38 us where this takes 33.  Rows in flight (2, 4), warps a block (2,
-// 4) and residency change nothing.  24 400 tokens of 8 heads, c = 128, bf16:
-// store 33 us (100 MB in, 27 out), fetch 27 us.
+// bytes.  What holds it: each warp loads one image, waits, converts and exits;
+// the first stall is the load (2.6 warps an issue in the store, 5.4 in the
+// fetch) with 60 % of the issue slots taken.  The store issues 200 instructions a
+// lane for 16 values (loads, maxima, E4M3 there and back, paired fmas and adds,
+// 16 shifts into the code words, six small stores); with 8 values a lane it
+// took 38 us where this takes 33.  Rows in flight (2, 4), warps a block (2, 4)
+// and residency change nothing; several images in flight a warp were not tried.
+// 24 400 tokens of 8 heads, c = 128, bf16: store 33 us (100 MB in, 27 out), fetch
+// 27 us; their bytes take 19 each.
 #include "api_check.h"
 #include "common.cuh"
 #include "kv4.cuh"

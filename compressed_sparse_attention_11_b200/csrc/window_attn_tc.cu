@@ -22,8 +22,10 @@
 //
 // Softmax: one thread per row (two warpgroups, one per query tile), running
 // maximum that moves only past 2^8 (the row of O is then rescaled in tensor
-// memory), weights rounded to bf16 for the second product while the sum takes
-// them unrounded; the arithmetic runs on pairs (fma.f32x2).  The softmax warps
+// memory), weights rounded to bf16 for the second product (whose operands have
+// one type, that of the values; the sum takes them unrounded: outputs are 0.0022
+// off the 64-bit result, where their own rounding alone makes 0.0017); the
+// arithmetic runs on pairs (fma.f32x2).  The softmax warps
 // take registers from the two others' warpgroup, so that a row of 128 scores
 // stays in registers.
 //
@@ -33,9 +35,10 @@
 // is S -> softmax (2200 cycles: 300 to read S, 300 for the maximum, 1450 for
 // exponentials that meet the other warpgroup's, 150 to store P) -> P.V -> next
 // S (1700 with the wait for the other tile's products): 3900, as P lives in S's
-// columns and the next S cannot start before P.V has read them (tensor memory
-// is full).  2 x 8192 tokens, 32 heads over 8, W = 1024, 4 first tokens,
-// C = 128: 308 us, 840 TFLOP/s.
+// columns and the next S cannot start before P.V has read them (at C = 128
+// tensor memory is full; at C = 64 128 columns are not used).  2 x 8192 tokens,
+// 32 heads over 8, W = 1024, 4 first tokens, C = 128: 335 us in a sustained run
+// (770 TFLOP/s under the power cap), 308 in a short one.
 //
 // A value that is not finite would reach the queries that a mask hides it from
 // through 0 x inf in the second product.  Hidden keys exist only in the edge

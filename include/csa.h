@@ -25,7 +25,10 @@
  *   - Layout: dense row-major, innermost dimension last, no padding.  Tensor
  *     pointers must be 16-byte aligned.
  *   - Numbers: CSA_F32 / CSA_BF16 select the element type of the activation
- *     tensors; all arithmetic is fp32.  Biases, head weights and sinks are fp32.
+ *     tensors.  Arithmetic, sums and softmax statistics are fp32; with bf16
+ *     tensors the operands of matrix products (softmax weights among them) are
+ *     bf16 where an entry point says nothing else.  Biases, head weights and
+ *     sinks are fp32.
  *   - Positions are 0-based.  A query at position t may read the compressed
  *     entries s < floor((t+1)/m) ([Notes] section 3: (pos+1)//m entries are
  *     complete) and the raw window rows max(0, t-W+1) .. t.
@@ -452,8 +455,9 @@ csa_status csa_paged_decode_step(const csa_cache_desc* desc, const csa_paging* p
  *   nh = 0 or nkv = 0 leaves that tensor out (its pointers are ignored).
  * Needs c <= 512 (above 256: c % 16 == 0, and rope_dims % 16 == 0 in the
  * halves form), else CSA_ERR_UNSUPPORTED.
- * Strides: whole 16-byte units.  Norm, angle (double) and rotation in fp32,
- * one rounding to `dt`.
+ * Strides: whole 16-byte units.  Norm and rotation in fp32, one rounding to
+ * `dt`; an angle is pos times a 64-bit fixed-point fraction of a turn, modulo 1,
+ * cut to 2^-32 of a turn and to fp32 for its sine and cosine.
  * ------------------------------------------------------------------------ */
 typedef struct {
   const float* q_gamma; /* [c], or [nh][c] with per_head; NULL: no norm of q   */
@@ -487,7 +491,10 @@ csa_status csa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
  * Needs: separate values: bf16, c = 64 or 128, nh / nkv <= 128 and fewer than
  * 2^31 rows batch * n_q * nkv; shared rows: c % 32 == 0 and
  * c <= 512, fp32 or bf16 (64 heads x 512 on the tensor cores).  Else
- * CSA_ERR_UNSUPPORTED.  out must not overlap an input.
+ * CSA_ERR_UNSUPPORTED.  out must not overlap an input.  On the tensor cores
+ * (separate values, 64 x 512) the softmax weights are rounded to bf16 for their
+ * product with the values, their sum takes them unrounded.  Keys and values
+ * that a query does not see may be anything.
  * ------------------------------------------------------------------------ */
 csa_status csa_window_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                            const void* v, int64_t v_stride, int64_t window, int64_t first,
