@@ -169,14 +169,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Whether a mask hides a key of tile tj from a row of query tile q.
-__device__ __forceinline__ bool edge_tile(const WinArgs& a, const Job& j, int q, int tj) {
-  const int ta = j.t0 + q * a.tt, tb = min(ta + a.tt - 1, j.t1), base = j.base(tj);
-  return base + kKeys - 1 > ta || tb - a.window + 1 > base;
-}
-// Whether its values are looked through: an edge tile of a query tile that needs it.
-__device__ __forceinline__ bool scanned(const WinArgs& a, const Job& j, const Need (&need)[2], int tj) {
-  return (need[0].has(tj) && edge_tile(a, j, 0, tj)) || (need[1].has(tj) && edge_tile(a, j, 1, tj));
+// The edge tiles among those a query tile needs: from `causal` on keys lie behind
+// a row's token, from `first` to `lower` before a row's window (the tiles below
+// hold nothing but first tokens: none is hidden, so however many first tokens
+// there are, the edge tiles are a few).
+struct Edges {
+  Need need;
+  int causal, first, lower;
+  __device__ bool has(int t) const { return need.has(t) && (t >= causal || (t >= first && t < lower)); }
+};
+__device__ __forceinline__ Edges edges_of(const WinArgs& a, const Job& j, int q) {
+  const int ta = j.t0 + q * a.tt, tb = min(ta + a.tt - 1, j.t1), v0 = j.base(0);
+  Edges e;
+  e.need = need_of(a, j, q);
+  e.causal = (ta - v0 + 1) / kKeys;
+  e.first = a.first / kKeys;
+  e.lower = (max(0, tb - a.window + 1 - v0) + kKeys - 1) / kKeys;
+  return e;
 }
 // Largest magnitudes of the upper and lower bf16 values of four words.
 __device__ __forceinline__ uint32_t tops(const uint4& x) {
@@ -193,9 +202,10 @@ __device__ __forceinline__ bool not_finite(uint32_t top) {
 template <int C>
 __device__ __noinline__ void add_odd_values(const WinArgs& a, const Job& j, int q, int t, uint32_t o_addr) {
   const int lane = threadIdx.x & 31;
-  const Need need[2] = {need_of(a, j, 0), need_of(a, j, 1)};
+  const Need need = need_of(a, j, q);
+  const Edges e0 = edges_of(a, j, 0), e1 = edges_of(a, j, 1);
   for (int tj = 0; tj < j.tiles; ++tj) {
-    if (!need[q].has(tj) || !scanned(a, j, need, tj)) continue;
+    if (!need.has(tj) || !(e0.has(tj) || e1.has(tj))) continue;
 #pragma unroll 1
     for (int d = 0; d < C; d += 32) {
       uint32_t o[32];
@@ -453,11 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_attn_kernel(
     bool ok = true;
     for (int w = blockIdx.x; w < a.works && ok; w += gridDim.x) {
       const Job jb = job_of(a, w);
-      const Need need[2] = {need_of(a, jb, 0), need_of(a, jb, 1)};
+      const Edges e0 = edges_of(a, jb, 0), e1 = edges_of(a, jb, 1);
       for (int tj = 0; tj < jb.tiles; ++tj, ++n) {
         const int st = n % kStages;
         if (!(ok = mbar_wait(&bar->v_full[st], (uint32_t)((n / kStages) & 1), err))) break;
-        if (scanned(a, jb, need, tj)) {
+        if (e0.has(tj) || e1.has(tj)) {
           uint4* x = reinterpret_cast<uint4*>(smem + F::off_v + st * F::kTileBytes) +
                      (warp - kScanWarp) * kPer * 32 + lane;
           uint32_t top = 0;

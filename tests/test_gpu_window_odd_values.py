@@ -92,3 +92,19 @@ def test_a_seen_infinity_costs_nothing_and_a_padded_batch_little():
     padded[0, 12000:] = float("nan")
     assert timed(call(padded), 5) < 4 * base + 5
     csa.csa_check()
+
+
+def test_many_first_tokens():
+    """An infinite value among 12000 first tokens, seen by every later query: no
+    tile of theirs hides a key, so the call takes what it takes without."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v = (torch.randn((1, 16384, h, 64), generator=g, device=DEV).bfloat16() for h in (8, 2, 2))
+    call = lambda x: (lambda: csa.csa_window_attn(q, k, x, 128, 12000, None, 0.1))  # noqa: E731
+    base = timed(call(v), 5)
+    seen = v.clone()
+    seen[0, 300, 1, 9] = INF
+    assert timed(call(seen), 5) < 2 * base + 1
+    out, clean = call(seen)(), call(v)()
+    assert bool(torch.isinf(out[0, 300:, 4:, 9]).all()) and torch.equal(out[..., :9], clean[..., :9])
+    assert torch.equal(out[0, :, :4], clean[0, :, :4]) and torch.equal(out[0, :256], clean[0, :256])
+    csa.csa_check()
